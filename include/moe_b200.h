@@ -29,6 +29,12 @@
  *                       [mlx-native DenseMatmulIdShape expert_stride_bytes]
  *  - moe_ffn_slots      the FFN's per-slot rows before the weights and the
  *                       combine (for proofs of the balanced/skewed identity)
+ *  - moe_layer_decode   the whole layer for a few tokens: router projection,
+ *                       routing, experts, combine and the optional shared
+ *                       expert in two kernels
+ *  - moe_matmul_lora    y[t] = W x[t] + scales[a] B[a] (A[a] x[t]), a =
+ *                       adapter_ids[t]: a shared projection with the low-rank
+ *                       adapter of each token's request beside it
  *  - moe_matmul_id_noalloc   decode-size moe_matmul_id without a workspace
  *  - moe_ep_dispatch / moe_ep_combine   the device halves of an
  *                       expert-parallel layer step over G ranks (the
@@ -305,6 +311,84 @@ MOE_API moe_status_t moe_ffn_forward_shared(
     void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * The whole layer for a few tokens (a decode step), from the hidden states to
+ * the layer's output, in two kernels:
+ *     logits = x . W_router^T, ids / weights as moe_route_topk computes them
+ *     y[t]   = sum_j weights[t, j] * d_j (in slot order), d_j as in moe_ffn_forward
+ *              [+ sigmoid(w_sh . x[t]) * shared expert, as in moe_ffn_forward_shared]
+ *   x        bf16 [m, hidden]
+ *   W_router bf16 [n_experts, hidden]; bias f32 [n_experts] or NULL
+ *   W_gate, W_up  bf16 [n_experts, inter, hidden]; W_down bf16 [n_experts, hidden, inter]
+ *   w_sh bf16 [hidden], W_sh_gate, W_sh_up bf16 [inter_sh, hidden],
+ *   W_sh_down bf16 [hidden, inter_sh]: the shared expert; without one pass
+ *            inter_sh = 0 and four NULLs
+ *   y        f32 [m, hidden] (out)
+ *   ids      int32 [m, top_k] (out); weights f32 [m, top_k] (out)
+ *   logits   f32 [m, n_experts] (out)
+ *   ws       moe_layer_decode_workspace() bytes, 256-byte aligned, no
+ *            initialisation needed; calls that may overlap on the GPU need
+ *            workspaces of their own
+ * 1 <= m <= MOE_LAYER_DECODE_MAX_TOKENS and m * top_k <=
+ * MOE_LAYER_DECODE_MAX_ROWS (else MOE_ERR_UNSUPPORTED_SHAPE: larger batches
+ * take moe_router_topk and moe_ffn_forward_shared); hidden, inter and inter_sh
+ * are multiples of 8.
+ * The logits are sums in f64, rounded once to f32, so which experts are
+ * chosen does not depend on the order of the additions; moe_router_topk adds
+ * in f32, and its choice can differ where two keys are that close.  The
+ * activation is kept to 24 bits (three bf16 parts), the sums in f32.  NaN or
+ * infinite inputs make the values that depend on them non-finite (a token's
+ * row depends on that token alone); no range error is raised.
+ * The second kernel is a cooperative launch of one block per SM with one grid
+ * barrier inside; a barrier that does not complete within the wait limit sets
+ * MOE_ERR_DEVICE_TIMEOUT in the status word (y is then not complete).
+ */
+#define MOE_LAYER_DECODE_MAX_TOKENS 32
+#define MOE_LAYER_DECODE_MAX_ROWS 256
+MOE_API size_t moe_layer_decode_workspace(int32_t m, int32_t hidden, int32_t inter,
+                                          int32_t inter_sh, int32_t top_k, int32_t n_experts);
+MOE_API moe_status_t moe_layer_decode(
+    const moe_bf16_t *x, const moe_bf16_t *W_router, const float *bias, const moe_bf16_t *W_gate,
+    const moe_bf16_t *W_up, const moe_bf16_t *W_down, const moe_bf16_t *w_sh,
+    const moe_bf16_t *W_sh_gate, const moe_bf16_t *W_sh_up, const moe_bf16_t *W_sh_down, float *y,
+    int32_t *ids, float *weights, float *logits, int32_t m, int32_t hidden, int32_t inter,
+    int32_t inter_sh, int32_t top_k, int32_t n_experts, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A projection that all tokens share, with low-rank adapters of many requests
+ * at once beside it:
+ *   y[t] = W . x[t] + scales[a] * B[a] . (A[a] . x[t]),   a = adapter_ids[t]
+ *   y[t] = W . x[t]                                        where a = -1
+ *   x    bf16 [m, k];  W bf16 [n, k]
+ *   adapter_ids int32 [m] in [-1, n_adapters), any order, any repetition
+ *   A    bf16 [n_adapters, rank, k];  B bf16 [n_adapters, n, rank]
+ *   scales f32 [n_adapters] or NULL (all 1)
+ *   y    [m, n] (out), f32 (y_dtype MOE_DTYPE_F32) or bf16 (MOE_DTYPE_BF16,
+ *        the f32 result rounded once)
+ *   ws   moe_matmul_lora_workspace() bytes, 256-byte aligned, no
+ *        initialisation needed; calls that may overlap on the GPU need
+ *        workspaces of their own
+ * k and rank are multiples of 8, rank <= MOE_MAX_LORA_RANK (an adapter of
+ * lower rank is padded with zero rows of A), 1 <= n <= 2^20, 1 <= n_adapters
+ * <= MOE_MAX_ADAPTERS, m <= 2^24.  x, W, A, B and y are 16-byte aligned.
+ * A row depends on its own token and adapter alone: NaN or infinities in
+ * another adapter, or in another row of x, do not reach it.
+ * An id out of range sets MOE_ERR_DEVICE_BAD_ID in the ws status word
+ * (moe_check_status) and leaves y unwritten.
+ */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+#define MOE_MAX_LORA_RANK 128
+#define MOE_MAX_ADAPTERS 65536
+MOE_API size_t moe_matmul_lora_workspace(int32_t m, int32_t n, int32_t k, int32_t rank,
+                                         int32_t n_adapters);
+MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t *x, const moe_bf16_t *W,
+                                     const int32_t *adapter_ids, const moe_bf16_t *A,
+                                     const moe_bf16_t *B, const float *scales, void *y,
+                                     int32_t y_dtype, int32_t m, int32_t n, int32_t k,
+                                     int32_t rank, int32_t n_adapters, void *ws, size_t ws_bytes,
+                                     void *stream);
+
+/*
  * Matmul by expert id without a workspace, for callers that cannot allocate
  * device memory (a plugin whose host runtime owns every allocation, a decode
  * loop that must never enter the driver's allocator).  The source pages have
@@ -404,7 +488,8 @@ MOE_API moe_status_t moe_set_stage_events(void *const *events, int32_t n_events)
 
 /*
  * Reads the device status word of a workspace used by moe_expert_map,
- * moe_matmul_id or moe_ffn_forward (synchronises `stream`).  Returns MOE_OK,
+ * moe_matmul_id, moe_ffn_forward, moe_layer_decode or moe_matmul_lora
+ * (synchronises `stream`).  Returns MOE_OK,
  * MOE_ERR_DEVICE_BAD_ID or MOE_ERR_DEVICE_TIMEOUT.
  */
 MOE_API moe_status_t moe_check_status(const void *ws, void *stream);

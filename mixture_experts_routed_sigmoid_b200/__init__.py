@@ -20,6 +20,10 @@ Functions keep the C names:
 * ``moe_ffn_slots(x, ids, W_gate, W_up, W_down)`` -> unweighted per-slot rows ``[m, top_k, hidden]``
 * ``moe_ffn_forward_shared(..., w_sh, W_sh_gate, W_sh_up, W_sh_down)`` -> the same plus the
   sigmoid-gated shared expert
+* ``moe_layer_decode(x, W_router, bias, top_k, W_gate, W_up, W_down[, w_sh, W_sh_gate, W_sh_up,
+  W_sh_down])`` -> ``(y, ids, weights, logits)``: the whole layer for a few tokens in two kernels
+* ``moe_matmul_lora(x, W, adapter_ids, A, B, scales)`` -> ``y [m, n]``: a shared projection with the
+  low-rank adapter of each token's request beside it
 * ``moe_ep_dispatch(x, ids, n_experts, n_ranks)`` / ``moe_ep_combine(d_back, weights, n_ranks, ws)``
   -> the device halves of an expert-parallel step (``ep.py`` drives the exchange)
 """
@@ -64,6 +68,10 @@ SIGNATURES = {
                       ctypes.c_int),
     "moe_ffn_shared_workspace": ([_I32, _I32, _I32, _I32, _I32, _I32], _SZ),
     "moe_ffn_forward_shared": ([_P] * 11 + [_I32] * 6 + [_P, _SZ, _P], ctypes.c_int),
+    "moe_layer_decode_workspace": ([_I32] * 6, _SZ),
+    "moe_layer_decode": ([_P] * 14 + [_I32] * 6 + [_P, _SZ, _P], ctypes.c_int),
+    "moe_matmul_lora_workspace": ([_I32] * 5, _SZ),
+    "moe_matmul_lora": ([_P] * 7 + [_I32] * 6 + [_P, _SZ, _P], ctypes.c_int),
     "moe_matmul_id_noalloc": ([_P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P],
                               ctypes.c_int),
     "moe_matmul_id_noalloc_status": ([_P], ctypes.c_int),
@@ -129,6 +137,12 @@ def _require(t: torch.Tensor, name: str, dtype, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _require_shape(t: torch.Tensor, name: str, dtype, device, shape):
+    _require(t, name, dtype, device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -358,6 +372,125 @@ def moe_ffn_forward_shared(x: torch.Tensor, ids: torch.Tensor, weights: torch.Te
         _ptr(x), _ptr(ids), _ptr(weights), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(w_sh),
         _ptr(W_sh_gate), _ptr(W_sh_up), _ptr(W_sh_down), _ptr(y), m, hidden, inter, inter_sh,
         top_k, n_experts, _ptr(ws), ws.numel(), _stream(dev)))
+    return y
+
+
+def moe_layer_decode_workspace(m, hidden, inter, inter_sh, top_k, n_experts) -> int:
+    return int(load_library().moe_layer_decode_workspace(m, hidden, inter, inter_sh, top_k,
+                                                         n_experts))
+
+
+def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor | None,
+                     top_k: int, W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor,
+                     w_sh: torch.Tensor | None = None, W_sh_gate: torch.Tensor | None = None,
+                     W_sh_up: torch.Tensor | None = None, W_sh_down: torch.Tensor | None = None,
+                     y: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+                     weights: torch.Tensor | None = None, logits: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None):
+    """The whole layer for at most 32 tokens in two kernels: router projection, routing, the
+    chosen experts' SwiGLU FFN, the weighted combine and, when its four weights are given, the
+    sigmoid-gated shared expert; returns ``(y [m, hidden] f32, ids, weights, logits)``."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    _require(x, "x", bf16)
+    dev = x.device
+    m, hidden = x.shape
+    _require(W_gate, "W_gate", bf16, dev)
+    n_experts, inter, _ = W_gate.shape
+    _require_shape(W_router, "W_router", bf16, dev, (n_experts, hidden))
+    _require_shape(W_gate, "W_gate", bf16, dev, (n_experts, inter, hidden))
+    _require_shape(W_up, "W_up", bf16, dev, (n_experts, inter, hidden))
+    _require_shape(W_down, "W_down", bf16, dev, (n_experts, hidden, inter))
+    if bias is not None:
+        _require_shape(bias, "bias", f32, dev, (n_experts,))
+    inter_sh = 0
+    shared = (w_sh, W_sh_gate, W_sh_up, W_sh_down)
+    if any(t is not None for t in shared):
+        if any(t is None for t in shared):
+            raise ValueError("a shared expert needs w_sh, W_sh_gate, W_sh_up and W_sh_down")
+        _require(W_sh_gate, "W_sh_gate", bf16, dev)
+        inter_sh = W_sh_gate.shape[0]
+        if inter_sh == 0:
+            raise ValueError("the shared expert has no rows")
+        _require_shape(w_sh, "w_sh", bf16, dev, (hidden,))
+        _require_shape(W_sh_gate, "W_sh_gate", bf16, dev, (inter_sh, hidden))
+        _require_shape(W_sh_up, "W_sh_up", bf16, dev, (inter_sh, hidden))
+        _require_shape(W_sh_down, "W_sh_down", bf16, dev, (hidden, inter_sh))
+    if y is None:
+        y = torch.empty((m, hidden), dtype=f32, device=dev)
+    else:
+        _require_shape(y, "y", f32, dev, (m, hidden))
+    if ids is None:
+        ids = torch.empty((m, top_k), dtype=torch.int32, device=dev)
+    else:
+        _require_shape(ids, "ids", torch.int32, dev, (m, top_k))
+    if weights is None:
+        weights = torch.empty((m, top_k), dtype=f32, device=dev)
+    else:
+        _require_shape(weights, "weights", f32, dev, (m, top_k))
+    if logits is None:
+        logits = torch.empty((m, n_experts), dtype=f32, device=dev)
+    else:
+        _require_shape(logits, "logits", f32, dev, (m, n_experts))
+    lib = load_library()
+    if ws is None:
+        ws = torch.empty(max(1, int(lib.moe_layer_decode_workspace(m, hidden, inter, inter_sh, top_k,
+                                                                   n_experts))),
+                         dtype=torch.uint8, device=dev)
+    else:
+        _require(ws, "ws", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_layer_decode(
+            _ptr(x), _ptr(W_router), _ptr(bias), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(w_sh),
+            _ptr(W_sh_gate), _ptr(W_sh_up), _ptr(W_sh_down), _ptr(y), _ptr(ids), _ptr(weights),
+            _ptr(logits), m, hidden, inter, inter_sh, top_k, n_experts, _ptr(ws), ws.numel(),
+            _stream(dev)))
+    return y, ids, weights, logits
+
+
+def moe_matmul_lora_workspace(m, n, k, rank, n_adapters) -> int:
+    return int(load_library().moe_matmul_lora_workspace(m, n, k, rank, n_adapters))
+
+
+_Y_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def moe_matmul_lora(x: torch.Tensor, W: torch.Tensor, adapter_ids: torch.Tensor, A: torch.Tensor,
+                    B: torch.Tensor, scales: torch.Tensor | None = None,
+                    out_dtype: torch.dtype = torch.float32, y: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None):
+    """``y[t] = W @ x[t] + scales[a] * B[a] @ (A[a] @ x[t])`` with ``a = adapter_ids[t]`` (-1: the
+    projection alone); returns ``[m, n]`` in ``out_dtype`` (f32 or bf16; that of ``y`` if given)."""
+    bf16 = torch.bfloat16
+    _require(x, "x", bf16)
+    dev = x.device
+    m, k = x.shape
+    _require(A, "A", bf16, dev)
+    n_adapters, rank, _ = A.shape
+    n = W.shape[0]
+    _require_shape(W, "W", bf16, dev, (n, k))
+    _require_shape(A, "A", bf16, dev, (n_adapters, rank, k))
+    _require_shape(B, "B", bf16, dev, (n_adapters, n, rank))
+    _require_shape(adapter_ids, "adapter_ids", torch.int32, dev, (m,))
+    if scales is not None:
+        _require_shape(scales, "scales", torch.float32, dev, (n_adapters,))
+    if y is not None:
+        out_dtype = y.dtype
+    if out_dtype not in _Y_DTYPES:
+        raise TypeError(f"the output must be torch.float32 or torch.bfloat16, got {out_dtype}")
+    if y is None:
+        y = torch.empty((m, n), dtype=out_dtype, device=dev)
+    else:
+        _require_shape(y, "y", out_dtype, dev, (m, n))
+    lib = load_library()
+    if ws is None:
+        ws = torch.empty(max(1, int(lib.moe_matmul_lora_workspace(m, n, k, rank, n_adapters))),
+                         dtype=torch.uint8, device=dev)
+    else:
+        _require(ws, "ws", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        _check(lib.moe_matmul_lora(_ptr(x), _ptr(W), _ptr(adapter_ids), _ptr(A), _ptr(B),
+                                   _ptr(scales), _ptr(y), _Y_DTYPES[out_dtype], m, n, k, rank,
+                                   n_adapters, _ptr(ws), ws.numel(), _stream(dev)))
     return y
 
 

@@ -804,6 +804,242 @@ MOE_API moe_status_t moe_ffn_forward_shared(
 
 namespace {
 
+// Status word, grid-barrier counter, the router's scores and shared gate, then
+// the activation of the routed rows and of the shared expert's (three bf16
+// parts each).
+struct LayerDecodeLayout {
+    size_t status, barrier, scores, gate, act, act_sh, end;
+};
+
+LayerDecodeLayout layer_decode_layout(int m, int inter, int inter_sh, int top_k, int n_experts) {
+    Carver c;
+    LayerDecodeLayout L;
+    L.status = c.take(sizeof(int));
+    L.barrier = c.take(sizeof(unsigned));
+    L.scores = c.take(sizeof(float) * m * n_experts);
+    L.gate = c.take(sizeof(float) * m);
+    L.act = c.take(sizeof(uint16_t) * 3 * static_cast<size_t>(m) * top_k * inter);
+    L.act_sh = c.take(sizeof(uint16_t) * 3 * static_cast<size_t>(m) * inter_sh);
+    L.end = c.off;
+    return L;
+}
+
+moe_status_t check_layer_decode_shape(int m, int hidden, int inter, int inter_sh, int top_k,
+                                      int n_experts) {
+    MOE_TRY(check_routing_shape(m, n_experts, top_k));
+    if (m > MOE_LAYER_DECODE_MAX_TOKENS || m * top_k > MOE_LAYER_DECODE_MAX_ROWS)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE,
+                    "at most %d tokens and %d routed rows (got %d and %d): larger batches take "
+                    "moe_router_topk and moe_ffn_forward_shared",
+                    MOE_LAYER_DECODE_MAX_TOKENS, MOE_LAYER_DECODE_MAX_ROWS, m, m * top_k);
+    MOE_TRY(check_k(hidden, "hidden"));
+    MOE_TRY(check_k(inter, "inter"));
+    if (inter_sh != 0) MOE_TRY(check_k(inter_sh, "inter_sh"));
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+MOE_API size_t moe_layer_decode_workspace(int32_t m, int32_t hidden, int32_t inter,
+                                          int32_t inter_sh, int32_t top_k, int32_t n_experts) {
+    if (check_layer_decode_shape(m, hidden, inter, inter_sh, top_k, n_experts) != MOE_OK) return 0;
+    return layer_decode_layout(m, inter, inter_sh, top_k, n_experts).end;
+}
+
+MOE_API moe_status_t moe_layer_decode(
+    const moe_bf16_t* x, const moe_bf16_t* W_router, const float* bias, const moe_bf16_t* W_gate,
+    const moe_bf16_t* W_up, const moe_bf16_t* W_down, const moe_bf16_t* w_sh,
+    const moe_bf16_t* W_sh_gate, const moe_bf16_t* W_sh_up, const moe_bf16_t* W_sh_down, float* y,
+    int32_t* ids, float* weights, float* logits, int32_t m, int32_t hidden, int32_t inter,
+    int32_t inter_sh, int32_t top_k, int32_t n_experts, void* ws, size_t ws_bytes, void* stream) {
+    MOE_TRY(check_layer_decode_shape(m, hidden, inter, inter_sh, top_k, n_experts));
+    if (m == 0) return ok();
+    MOE_TRY(check_ptr(x, "x", 16));
+    MOE_TRY(check_ptr(W_router, "W_router", 16));
+    if (bias) MOE_TRY(check_ptr(bias, "bias", 4));
+    MOE_TRY(check_ptr(W_gate, "W_gate", 16));
+    MOE_TRY(check_ptr(W_up, "W_up", 16));
+    MOE_TRY(check_ptr(W_down, "W_down", 16));
+    if (inter_sh) {
+        MOE_TRY(check_ptr(w_sh, "w_sh", 16));
+        MOE_TRY(check_ptr(W_sh_gate, "W_sh_gate", 16));
+        MOE_TRY(check_ptr(W_sh_up, "W_sh_up", 16));
+        MOE_TRY(check_ptr(W_sh_down, "W_sh_down", 16));
+    } else if (w_sh || W_sh_gate || W_sh_up || W_sh_down) {
+        return fail(MOE_ERR_INVALID_ARGUMENT, "shared expert weights need inter_sh > 0");
+    }
+    MOE_TRY(check_ptr(y, "y", 16));
+    MOE_TRY(check_ptr(ids, "ids", 4));
+    MOE_TRY(check_ptr(weights, "weights", 4));
+    MOE_TRY(check_ptr(logits, "logits", 4));
+    const LayerDecodeLayout L = layer_decode_layout(m, inter, inter_sh, top_k, n_experts);
+    MOE_TRY(check_ws(ws, ws_bytes, L.end));
+    char* wsb = static_cast<char*>(ws);
+    const auto bf = [](const moe_bf16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
+    moe::LayerDecodeArgs a{};
+    a.x = bf(x);
+    a.W_gate = bf(W_gate);
+    a.W_up = bf(W_up);
+    a.W_down = bf(W_down);
+    a.S_gate = bf(W_sh_gate);
+    a.S_up = bf(W_sh_up);
+    a.S_down = bf(W_sh_down);
+    a.bias = bias;
+    a.scores = reinterpret_cast<float*>(wsb + L.scores);
+    a.gate = reinterpret_cast<float*>(wsb + L.gate);
+    a.act = reinterpret_cast<__nv_bfloat16*>(wsb + L.act);
+    a.act_sh = reinterpret_cast<__nv_bfloat16*>(wsb + L.act_sh);
+    a.y = y;
+    a.ids = ids;
+    a.weights = weights;
+    a.barrier = reinterpret_cast<unsigned*>(wsb + L.barrier);
+    a.status = reinterpret_cast<int*>(wsb + L.status);
+    a.m = m;
+    a.hidden = hidden;
+    a.inter = inter;
+    a.inter_sh = inter_sh;
+    a.top_k = top_k;
+    a.n_experts = n_experts;
+    a.wait_limit_ns = moe::kDefaultWaitLimitNs;
+    const cudaError_t err = moe::launch_layer_decode(a, bf(W_router), bf(w_sh), logits, num_sms(),
+                                                     static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return cuda_fail(err, "layer launch");
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// K ranges of the adapters' first product: enough blocks (32 tokens x 32
+// adapter rows x one range each) to occupy the SMs, at least two steps of a
+// block's 16 warps per range.  A function of the shape alone.
+int lora_k_splits(long long m, int k, int rank) {
+    const long long blocks = ((m + 31) / 32) * ((rank + 31) / 32);
+    const long long by_sms = blocks > 0 ? 148 / blocks : 1;
+    const long long by_k = k / 2048;
+    const long long s = by_sms < by_k ? by_sms : by_k;
+    return s < 1 ? 1 : s > 8 ? 8 : static_cast<int>(s);
+}
+
+// Status word, the partial sums h [k_splits, m, rank], and for the larger
+// batches the projection [m, n] f32 before the adapters' part is added.
+struct LoraLayout {
+    size_t status, h, base, end;
+    int k_splits;
+};
+
+LoraLayout lora_layout(long long m, int n, int k, int rank) {
+    Carver c;
+    LoraLayout L;
+    L.k_splits = lora_k_splits(m, k, rank);
+    L.status = c.take(sizeof(int));
+    L.h = c.take(sizeof(float) * L.k_splits * static_cast<size_t>(m) * rank);
+    L.base = c.take(m > moe::kLoraStreamMaxTokens ? sizeof(float) * static_cast<size_t>(m) * n : 0);
+    L.end = c.off;
+    return L;
+}
+
+moe_status_t check_lora_shape(long long m, int n, int k, int rank, int n_adapters) {
+    if (m < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "m must be >= 0 (got %lld)", m);
+    if (m > MOE_MAX_ROUTED_ROWS)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "m must be <= %d (got %lld)", MOE_MAX_ROUTED_ROWS, m);
+    if (n < 1 || n > (1 << 20))
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n must be in [1, 2^20] (got %d)", n);
+    MOE_TRY(check_k(k, "k"));
+    MOE_TRY(check_k(rank, "rank"));
+    if (rank > MOE_MAX_LORA_RANK)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rank must be <= %d (got %d)", MOE_MAX_LORA_RANK, rank);
+    if (n_adapters < 1 || n_adapters > MOE_MAX_ADAPTERS)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_adapters must be in [1, %d] (got %d)",
+                    MOE_MAX_ADAPTERS, n_adapters);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+MOE_API size_t moe_matmul_lora_workspace(int32_t m, int32_t n, int32_t k, int32_t rank,
+                                         int32_t n_adapters) {
+    if (check_lora_shape(m, n, k, rank, n_adapters) != MOE_OK) return 0;
+    return lora_layout(m, n, k, rank).end;
+}
+
+MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
+                                     const int32_t* adapter_ids, const moe_bf16_t* A,
+                                     const moe_bf16_t* B, const float* scales, void* y,
+                                     int32_t y_dtype, int32_t m, int32_t n, int32_t k,
+                                     int32_t rank, int32_t n_adapters, void* ws, size_t ws_bytes,
+                                     void* stream) {
+    MOE_TRY(check_lora_shape(m, n, k, rank, n_adapters));
+    if (y_dtype != MOE_DTYPE_F32 && y_dtype != MOE_DTYPE_BF16)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "y_dtype must be 0 (f32) or 1 (bf16) (got %d)", y_dtype);
+    if (m == 0) return ok();
+    MOE_TRY(check_ptr(x, "x", 16));
+    MOE_TRY(check_ptr(W, "W", 16));
+    MOE_TRY(check_ptr(adapter_ids, "adapter_ids", 4));
+    MOE_TRY(check_ptr(A, "A", 16));
+    MOE_TRY(check_ptr(B, "B", 16));
+    if (scales) MOE_TRY(check_ptr(scales, "scales", 4));
+    MOE_TRY(check_ptr(y, "y", 16));
+    const LoraLayout L = lora_layout(m, n, k, rank);
+    MOE_TRY(check_ws(ws, ws_bytes, L.end));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* wsb = static_cast<char*>(ws);
+    const auto bf = [](const moe_bf16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
+    moe::LoraArgs a{};
+    a.x = bf(x);
+    a.W = bf(W);
+    a.adapter_ids = adapter_ids;
+    a.A = bf(A);
+    a.B = bf(B);
+    a.scales = scales;
+    a.h = reinterpret_cast<float*>(wsb + L.h);
+    a.y = y;
+    a.status = reinterpret_cast<int*>(wsb + L.status);
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.rank = rank;
+    a.n_adapters = n_adapters;
+    a.k_splits = L.k_splits;
+    a.y_dtype = y_dtype;
+    cudaError_t err = moe::launch_lora_shrink(a, s);
+    if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
+    if (m <= moe::kLoraStreamMaxTokens) {
+        err = moe::launch_lora_stream(a, num_sms(), s);
+        if (err != cudaSuccess) return cuda_fail(err, "streaming projection launch");
+        return ok();
+    }
+    CUtensorMap map_x, map_w;
+    MOE_TRY(make_map(&map_x, x, k, m, 128, "x"));
+    MOE_TRY(make_map(&map_w, W, k, n, 256, "W"));
+    float* base = reinterpret_cast<float*>(wsb + L.base);
+    moe::GroupedGemmArgs g{};
+    g.out = base;
+    g.status = a.status;
+    g.status_out = a.status;
+    g.rows = m;
+    g.n = n;
+    g.k = k;
+    g.n_col_tiles = (n + 255) / 256;
+    g.dense_m_tiles = (m + moe::kTileRows - 1) / moe::kTileRows;
+    g.k_splits = 1;
+    g.wait_limit_ns = moe::kDefaultWaitLimitNs;
+    err = moe::launch_grouped_gemm(4, map_x, map_w, map_w, g, num_sms(), s);
+    if (err != cudaSuccess) return cuda_fail(err, "projection launch");
+    err = moe::launch_lora_add(a, base, num_sms(), s);
+    if (err != cudaSuccess) return cuda_fail(err, "adapter launch");
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
 // Dispatch workspace: the expert map over owner ranks (status word first),
 // then the owner rank of every routed row.
 struct EpLayout {

@@ -7,7 +7,27 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
+
+// Runs a set-up call (a shared-memory opt-in) until it has succeeded once on
+// the current device.
+struct PerDeviceOnce {
+    std::atomic<unsigned long long> done{0};  // bit d: device d
+    template <class F>
+    cudaError_t run(F f) {
+        int dev = 0;
+        cudaError_t err = cudaGetDevice(&dev);
+        if (err != cudaSuccess) return err;
+        const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+        if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        err = f();
+        if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return err;
+    }
+};
+
 
 // Routed rows per block of the expert-map count/scatter passes.
 constexpr int kMapChunkRows = 2048;
@@ -152,6 +172,50 @@ cudaError_t launch_ep_pack(const __nv_bfloat16* x, const int* ids, const int* pe
 cudaError_t launch_ep_combine(const float* d_back, const int* inv, const float* weights, float* y,
                               int m, int hidden, int top_k, const int* status,
                               cudaStream_t stream);
+
+// The whole layer for a few tokens: the router kernel (which resets status and
+// barrier), then the cooperative experts kernel.
+constexpr int kLayerDecodeMaxTokens = 32;
+constexpr int kLayerDecodeMaxRows = 256;
+struct LayerDecodeArgs {
+    const __nv_bfloat16* x;  // [m, hidden]
+    const __nv_bfloat16 *W_gate, *W_up, *W_down;
+    const __nv_bfloat16 *S_gate, *S_up, *S_down;  // shared expert (inter_sh > 0)
+    const float* bias;    // [n_experts] or null
+    const float* scores;  // [m, n_experts] sigmoid(logits), written by the router kernel
+    const float* gate;    // [m] the shared expert's gate, written by the router kernel
+    __nv_bfloat16* act;     // [m * top_k, 3, inter] activation as three bf16 parts, sorted rows
+    __nv_bfloat16* act_sh;  // [m, 3, inter_sh]
+    float* y;               // [m, hidden]
+    int* ids;               // [m, top_k]
+    float* weights;         // [m, top_k]
+    unsigned* barrier;
+    int* status;
+    int m, hidden, inter, inter_sh, top_k, n_experts;
+    unsigned long long wait_limit_ns;
+};
+cudaError_t launch_layer_decode(const LayerDecodeArgs& args, const __nv_bfloat16* W_router,
+                                const __nv_bfloat16* w_sh, float* logits, int num_sms,
+                                cudaStream_t stream);
+
+// Shared projection with per-token low-rank adapters.
+constexpr int kLoraStreamMaxTokens = 64;
+struct LoraArgs {
+    const __nv_bfloat16* x;  // [m, k]
+    const __nv_bfloat16* W;  // [n, k]
+    const int* adapter_ids;  // [m], -1: none
+    const __nv_bfloat16* A;  // [n_adapters, rank, k]
+    const __nv_bfloat16* B;  // [n_adapters, n, rank]
+    const float* scales;     // [n_adapters] or null
+    float* h;                // [k_splits, m, rank] partial sums of A x
+    void* y;                 // [m, n]
+    int* status;
+    long long m;
+    int n, k, rank, n_adapters, k_splits, y_dtype;
+};
+cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream);
+cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_lora_add(const LoraArgs& a, const float* base, int num_sms, cudaStream_t stream);
 
 // Sets the calling thread's moe_last_error() message.
 void set_last_error(const char* msg);
