@@ -140,9 +140,31 @@ def _require(t: torch.Tensor, name: str, dtype, device=None):
 
 
 def _require_shape(t: torch.Tensor, name: str, dtype, device, shape):
+    # the decode-step calls check up to 15 tensors each time: one cheap test
+    # for the good case, the reason only when it fails
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
+            and t.shape == shape and t.is_contiguous()):
+        return
     _require(t, name, dtype, device)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _run_on(device, fn, *args):
+    """Call an entry point on a device's current stream, with that device current."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, _raw_stream(index)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _raw_stream(index)))
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -394,7 +416,6 @@ def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor
     _require(x, "x", bf16)
     dev = x.device
     m, hidden = x.shape
-    _require(W_gate, "W_gate", bf16, dev)
     n_experts, inter, _ = W_gate.shape
     _require_shape(W_router, "W_router", bf16, dev, (n_experts, hidden))
     _require_shape(W_gate, "W_gate", bf16, dev, (n_experts, inter, hidden))
@@ -407,7 +428,6 @@ def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor
     if any(t is not None for t in shared):
         if any(t is None for t in shared):
             raise ValueError("a shared expert needs w_sh, W_sh_gate, W_sh_up and W_sh_down")
-        _require(W_sh_gate, "W_sh_gate", bf16, dev)
         inter_sh = W_sh_gate.shape[0]
         if inter_sh == 0:
             raise ValueError("the shared expert has no rows")
@@ -437,13 +457,12 @@ def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor
                                                                    n_experts))),
                          dtype=torch.uint8, device=dev)
     else:
-        _require(ws, "ws", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        _check(lib.moe_layer_decode(
-            _ptr(x), _ptr(W_router), _ptr(bias), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(w_sh),
-            _ptr(W_sh_gate), _ptr(W_sh_up), _ptr(W_sh_down), _ptr(y), _ptr(ids), _ptr(weights),
-            _ptr(logits), m, hidden, inter, inter_sh, top_k, n_experts, _ptr(ws), ws.numel(),
-            _stream(dev)))
+        _require_shape(ws, "ws", torch.uint8, dev, (ws.numel(),))
+    _run_on(dev, lib.moe_layer_decode, x.data_ptr(), W_router.data_ptr(), _ptr(bias),
+            W_gate.data_ptr(), W_up.data_ptr(), W_down.data_ptr(), _ptr(w_sh), _ptr(W_sh_gate),
+            _ptr(W_sh_up), _ptr(W_sh_down), y.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+            logits.data_ptr(), m, hidden, inter, inter_sh, top_k, n_experts, ws.data_ptr(),
+            ws.numel())
     return y, ids, weights, logits
 
 
@@ -464,7 +483,6 @@ def moe_matmul_lora(x: torch.Tensor, W: torch.Tensor, adapter_ids: torch.Tensor,
     _require(x, "x", bf16)
     dev = x.device
     m, k = x.shape
-    _require(A, "A", bf16, dev)
     n_adapters, rank, _ = A.shape
     n = W.shape[0]
     _require_shape(W, "W", bf16, dev, (n, k))
@@ -486,11 +504,10 @@ def moe_matmul_lora(x: torch.Tensor, W: torch.Tensor, adapter_ids: torch.Tensor,
         ws = torch.empty(max(1, int(lib.moe_matmul_lora_workspace(m, n, k, rank, n_adapters))),
                          dtype=torch.uint8, device=dev)
     else:
-        _require(ws, "ws", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        _check(lib.moe_matmul_lora(_ptr(x), _ptr(W), _ptr(adapter_ids), _ptr(A), _ptr(B),
-                                   _ptr(scales), _ptr(y), _Y_DTYPES[out_dtype], m, n, k, rank,
-                                   n_adapters, _ptr(ws), ws.numel(), _stream(dev)))
+        _require_shape(ws, "ws", torch.uint8, dev, (ws.numel(),))
+    _run_on(dev, lib.moe_matmul_lora, x.data_ptr(), W.data_ptr(), adapter_ids.data_ptr(),
+            A.data_ptr(), B.data_ptr(), _ptr(scales), y.data_ptr(), _Y_DTYPES[out_dtype], m, n, k,
+            rank, n_adapters, ws.data_ptr(), ws.numel())
     return y
 
 

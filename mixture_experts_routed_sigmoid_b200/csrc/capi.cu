@@ -804,14 +804,14 @@ MOE_API moe_status_t moe_ffn_forward_shared(
 
 namespace {
 
-// Status word, grid-barrier counter, the router's scores and shared gate, then
-// the activation of the routed rows and of the shared expert's (three bf16
-// parts each).
+// Status word, grid-barrier counter, the router's scores and shared gate, the
+// activation of the routed rows and of the shared expert's (three bf16 parts
+// each), then the down outputs of all of them (f32).
 struct LayerDecodeLayout {
-    size_t status, barrier, scores, gate, act, act_sh, end;
+    size_t status, barrier, scores, gate, act, act_sh, d, end;
 };
 
-LayerDecodeLayout layer_decode_layout(int m, int inter, int inter_sh, int top_k, int n_experts) {
+LayerDecodeLayout layer_decode_layout(int m, int hidden, int inter, int inter_sh, int top_k, int n_experts) {
     Carver c;
     LayerDecodeLayout L;
     L.status = c.take(sizeof(int));
@@ -820,6 +820,7 @@ LayerDecodeLayout layer_decode_layout(int m, int inter, int inter_sh, int top_k,
     L.gate = c.take(sizeof(float) * m);
     L.act = c.take(sizeof(uint16_t) * 3 * static_cast<size_t>(m) * top_k * inter);
     L.act_sh = c.take(sizeof(uint16_t) * 3 * static_cast<size_t>(m) * inter_sh);
+    L.d = c.take(sizeof(float) * static_cast<size_t>(m) * (top_k + (inter_sh > 0 ? 1 : 0)) * hidden);
     L.end = c.off;
     return L;
 }
@@ -845,7 +846,7 @@ extern "C" {
 MOE_API size_t moe_layer_decode_workspace(int32_t m, int32_t hidden, int32_t inter,
                                           int32_t inter_sh, int32_t top_k, int32_t n_experts) {
     if (check_layer_decode_shape(m, hidden, inter, inter_sh, top_k, n_experts) != MOE_OK) return 0;
-    return layer_decode_layout(m, inter, inter_sh, top_k, n_experts).end;
+    return layer_decode_layout(m, hidden, inter, inter_sh, top_k, n_experts).end;
 }
 
 MOE_API moe_status_t moe_layer_decode(
@@ -874,7 +875,7 @@ MOE_API moe_status_t moe_layer_decode(
     MOE_TRY(check_ptr(ids, "ids", 4));
     MOE_TRY(check_ptr(weights, "weights", 4));
     MOE_TRY(check_ptr(logits, "logits", 4));
-    const LayerDecodeLayout L = layer_decode_layout(m, inter, inter_sh, top_k, n_experts);
+    const LayerDecodeLayout L = layer_decode_layout(m, hidden, inter, inter_sh, top_k, n_experts);
     MOE_TRY(check_ws(ws, ws_bytes, L.end));
     char* wsb = static_cast<char*>(ws);
     const auto bf = [](const moe_bf16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };
@@ -891,6 +892,7 @@ MOE_API moe_status_t moe_layer_decode(
     a.gate = reinterpret_cast<float*>(wsb + L.gate);
     a.act = reinterpret_cast<__nv_bfloat16*>(wsb + L.act);
     a.act_sh = reinterpret_cast<__nv_bfloat16*>(wsb + L.act_sh);
+    a.d = reinterpret_cast<float*>(wsb + L.d);
     a.y = y;
     a.ids = ids;
     a.weights = weights;

@@ -112,6 +112,17 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, uint6
     }
 }
 
+// ------------------------------------------------- programmatic launch order
+// For a kernel launched with programmatic stream serialisation: the kernel
+// before it lets it start early, and it waits until that kernel has finished
+// and its writes are visible.
+__device__ __forceinline__ void allow_next_kernel() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- TMA
 // 2-D tiled bulk tensor copy global -> shared, completion on an mbarrier.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,

@@ -186,6 +186,7 @@ struct LayerDecodeArgs {
     const float* gate;    // [m] the shared expert's gate, written by the router kernel
     __nv_bfloat16* act;     // [m * top_k, 3, inter] activation as three bf16 parts, sorted rows
     __nv_bfloat16* act_sh;  // [m, 3, inter_sh]
+    float* d;               // [m * top_k + m, hidden] down outputs (larger batches)
     float* y;               // [m, hidden]
     int* ids;               // [m, top_k]
     float* weights;         // [m, top_k]

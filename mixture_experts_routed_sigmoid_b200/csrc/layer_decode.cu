@@ -14,19 +14,24 @@
 //   rounded logits are those of the exact sum but for ties of the rounding.
 // Kernel 2 (experts): a cooperative grid of one block per SM.  Every block
 //   repeats the routing of the few tokens (cheaper than a launch), takes an
-//   equal share of all active experts' gate/up rows, and after a grid barrier
-//   an equal share of the output's hidden rows over all active experts, so
-//   the weighted combine happens in its own shared memory, in slot order,
-//   with no atomics and no per-slot rows in global memory.
+//   equal share of all active experts' gate/up rows, then, after a grid
+//   barrier, a share of the down rows.  For m <= 8 that share is the block's
+//   own hidden rows of every active expert, so the weighted combine happens in
+//   its shared memory, in slot order.  Larger batches may crowd many tokens on
+//   one expert; re-reading all their activations in every block would then
+//   cost more L2 traffic than the weights, so a block takes consecutive rows
+//   of few experts instead, and the outputs d meet in global memory behind a
+//   second grid barrier (same sums, same slot order, no atomics).
 //
-// The bound is reading the distinct chosen experts' weights once.  Weight
-// rows go from global memory straight into mma.sync fragments
-// (stream_mma.cuh); the 16 warps of a block split K, and partial sums meet in
-// shared memory once per tile.  gate/up multiplies the bf16 x as it is; the
-// f32 activation enters the down projection as three bf16 parts, so nothing
-// is rounded below f32.
+// The bound is reading the distinct chosen experts' weights once; every warp
+// streams its own rows (stream_mma.cuh).  gate/up multiplies the bf16 x as it
+// is; the f32 activation enters the down projection as three bf16 parts, so
+// nothing is rounded below f32.  A row's K order is the same wherever it
+// lands, so its bits depend on its own token alone.
 #include <climits>
 #include <math.h>
+
+#include <type_traits>
 
 #include "launch.h"
 #include "stream_mma.cuh"
@@ -36,7 +41,6 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKb = 64;      // K columns of one warp step: 128 bytes of each weight row
 constexpr int kTileI = 16;   // intermediate rows of a gate/up tile (gate and up rows each)
 constexpr int kTileH = 32;   // hidden rows of a down tile
 constexpr int kMaxTokens = kLayerDecodeMaxTokens;
@@ -56,6 +60,9 @@ __global__ void __launch_bounds__(kThreads) layer_router_kernel(
     float* __restrict__ logits, float* __restrict__ scores, float* __restrict__ gate,
     unsigned* __restrict__ barrier, int* __restrict__ status) {
     __shared__ double part[kWarps][kRouterRows * kMaxTokens];
+    // the experts kernel may come onto the SMs as this one leaves them; it waits
+    // for this kernel's writes before it reads them
+    allow_next_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         *barrier = 0;  // of the kernel that follows
@@ -132,16 +139,20 @@ __global__ void __launch_bounds__(kThreads) layer_router_kernel(
 }
 
 // ----------------------------------------------------------------- experts
-// Dynamic shared memory of the experts kernel for NT token groups of 8.
-template <int NT>
+constexpr int kStages = 3;  // ring slots per warp: 2 steps in flight while one is used
+
 struct ExpertsSmem {
-    float red[2][kWarps][2 * NT * 4][32];  // partial sums of one tile, double buffered
-    float d[kMaxRows + kMaxTokens][kTileH + 1];  // d[routed row or shared token][hidden row]
-    int id[kMaxRows], perm[kMaxRows], gexp[kMaxRows], gfirst[kMaxRows], gcnt[kMaxRows];
+    unsigned char ring[kWarps][kStages][kRingBytes];  // first the routing keys, then weights
+    int key[kMaxRows], sorted[kMaxRows], perm[kMaxRows];
+    int gexp[kMaxRows], gfirst[kMaxRows + 1];
     int slot_id[kMaxRows];
     float weight[kMaxRows];
     int warp_n[kWarps], flag;
 };
+// The block-combining variant keeps the down outputs of its 32 hidden rows in
+// shared memory, [routed rows, then shared rows][hidden row], behind ExpertsSmem;
+// this many rows fit.
+constexpr int kCombineRows = (232448 - static_cast<int>(sizeof(ExpertsSmem))) / ((kTileH + 1) * 4);
 
 // Top-k of one token by (score + bias descending, expert ascending), by one
 // warp.  key: the warp's scratch of n_experts floats.  Each lane keeps the
@@ -156,14 +167,27 @@ __device__ __forceinline__ void route_token(const float* __restrict__ scores,
         const unsigned b = __float_as_uint(k);
         return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
     };
+    unsigned* k = reinterpret_cast<unsigned*>(key);
     unsigned best = 0;  // 0: nothing left (every real key is above it)
     int best_e = INT_MAX;
-    for (int e = lane; e < n_experts; e += 32) {
-        const unsigned u = ordered(scores[e] + (bias ? bias[e] : 0.0f));
-        reinterpret_cast<unsigned*>(key)[e] = u;
-        if (u > best) {
-            best = u;
-            best_e = e;
+    for (int e0 = lane; e0 < n_experts; e0 += 8 * 32) {  // eight loads at a time
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + 32 * i;
+            s[i] = e < n_experts ? scores[e] + (bias ? bias[e] : 0.0f) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + 32 * i;
+            const unsigned u = ordered(s[i]);
+            if (e < n_experts) {
+                k[e] = u;
+                if (u > best) {
+                    best = u;
+                    best_e = e;
+                }
+            }
         }
     }
     int my_e = 0;
@@ -173,15 +197,17 @@ __device__ __forceinline__ void route_token(const float* __restrict__ scores,
             __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(best_e) : 0xffffffffu));
         if (lane == j) my_e = win;
         if (best_e == win) {
-            unsigned* k = reinterpret_cast<unsigned*>(key);
             k[win] = 0;
             best = 0;
             best_e = INT_MAX;
-            for (int e = lane; e < n_experts; e += 32)
-                if (k[e] > best) {
-                    best = k[e];
+#pragma unroll 8
+            for (int e = lane; e < n_experts; e += 32) {
+                const unsigned u = k[e];
+                if (u > best) {
+                    best = u;
                     best_e = e;
                 }
+            }
         }
     }
     const float s = lane < top_k ? scores[my_e] : 0.0f;
@@ -194,18 +220,85 @@ __device__ __forceinline__ void route_token(const float* __restrict__ scores,
     __syncwarp();
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerDecodeArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    ExpertsSmem<NT>& sm = *reinterpret_cast<ExpertsSmem<NT>*>(smem_raw);
+// One warp's share of a phase.  The rows of all groups (`wid` rows for each
+// routed group, then wid_sh of the shared expert) are cut into tiles of `n`
+// rows, the last of a group with fewer.  All warps take one tile each per
+// round, so the grid reads one moving window of the weights (with a contiguous
+// range of tiles per warp the slowest SM took 1.5 times the fastest's time at
+// 6 GB of weights).  Within a round a block's warps take neighbouring tiles,
+// mostly of one expert, whose tokens they share in the L1.
+struct Share {
+    int pos;    // this warp's tile of the round, or past the end
+    int round;  // first tile of the round
+    int end;    // tiles
+    int n, per_group, wid, wid_sh;
+};
+
+struct Tile {
+    int q, r, n;       // group, first row within it, rows
+    int first, cnt;    // the group's tokens: sorted rows [first, first + cnt)
+    int expert;        // -1: the shared expert
+    const __nv_bfloat16 *w0, *w1;  // row r of gate and up (phase 1) or of down (w0)
+    int k;             // row length
+};
+
+// Expert map of the routed rows (rows <= kMaxRows): sm.perm lists them by
+// (expert, routed row); group q holds the rows of expert sm.gexp[q] at sorted
+// positions sm.gfirst[q] up to sm.gfirst[q + 1].  Returns the number of groups.
+__device__ __forceinline__ int map_rows(ExpertsSmem& sm, int rows) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c8 = (lane & 3) * 8;
+    static_assert(MOE_MAX_EXPERTS * kMaxRows <= INT_MAX, "sort keys");
+    const int mine = tid < rows ? sm.slot_id[tid] * kMaxRows + tid : INT_MAX;  // keys are distinct
+    if (tid < kMaxRows) sm.key[tid] = mine;
+    __syncthreads();
+    if (tid < rows) {
+        int rank = 0;
+        const int4* keys = reinterpret_cast<const int4*>(sm.key);
+#pragma unroll 4
+        for (int i = 0; i < (rows + 3) / 4; ++i) {
+            const int4 v = keys[i];
+            rank += (v.x < mine) + (v.y < mine) + (v.z < mine) + (v.w < mine);
+        }
+        sm.sorted[rank] = mine;
+        sm.perm[rank] = tid;
+    }
+    __syncthreads();
+    const int e = tid < rows ? sm.sorted[tid] / kMaxRows : -1;
+    const bool opens = tid < rows && (tid == 0 || sm.sorted[tid - 1] / kMaxRows != e);
+    const unsigned ballot = __ballot_sync(0xffffffffu, opens);
+    if (lane == 0) sm.warp_n[warp] = __popc(ballot);
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm.warp_n[w];
+        total += sm.warp_n[w];
+    }
+    if (opens) {
+        const int q = before + __popc(ballot & ((1u << lane) - 1u));
+        sm.gexp[q] = e;
+        sm.gfirst[q] = tid;
+    }
+    if (tid == 0) sm.gfirst[total] = rows;
+    __syncthreads();
+    return total;
+}
+
+template <int NT, bool COMBINE>
+__global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerDecodeArgs a) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    ExpertsSmem& sm = *reinterpret_cast<ExpertsSmem*>(smem_raw);
+    float(*sm_d)[kTileH + 1] = reinterpret_cast<float(*)[kTileH + 1]>(smem_raw + sizeof(ExpertsSmem));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
     const int rows = a.m * a.top_k;
     const int n_shared = a.inter_sh > 0 ? 1 : 0;
 
+    wait_for_previous_kernel();
     // routing and expert map of the few tokens, in every block
     {
-        float* keys = &sm.red[0][0][0][0] + warp * a.n_experts;  // of the warps that have tokens
+        float* keys = reinterpret_cast<float*>(&sm.ring[warp][0][0]);
+        static_assert(kStages * kRingBytes >= 4 * MOE_MAX_EXPERTS, "routing keys");
         for (int t = warp; t < a.m; t += kWarps)
             route_token(a.scores + static_cast<size_t>(t) * a.n_experts, a.bias, a.n_experts, a.top_k,
                         keys, sm.slot_id + t * a.top_k, sm.weight + t * a.top_k, lane);
@@ -216,223 +309,266 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
             a.ids[r] = sm.slot_id[r];
             a.weights[r] = sm.weight[r];
         }
-    int n_groups = 0;
-    block_small_map(sm.slot_id, rows, a.n_experts, sm.id, sm.perm, sm.gexp, sm.gfirst, sm.gcnt,
-                    sm.warp_n, &sm.flag, &n_groups);
+    const int n_groups = map_rows(sm, rows);
 
-    // Group q: expert sm.gexp[q] with the sorted rows [first, first + cnt);
-    // group n_groups: the shared expert with every token.
-    const auto group = [&](int q, int& first, int& cnt, int& expert) {
-        if (q < n_groups) {
-            first = sm.gfirst[q];
-            cnt = sm.gcnt[q];
-            expert = sm.gexp[q];
+    // Rows of the down phase: with COMBINE this block's own hidden rows
+    // [h_lo, h_hi) of every group, otherwise all hidden rows.
+    const int h_lo = COMBINE ? static_cast<int>(static_cast<long long>(a.hidden) * blockIdx.x / gridDim.x) : 0;
+    const int h_hi = COMBINE ? static_cast<int>(static_cast<long long>(a.hidden) * (blockIdx.x + 1) / gridDim.x)
+                             : a.hidden;
+
+    // h0: hidden row of row 0 (down)
+    const auto find_tile = [&](bool down, const Share& s, int h0) -> Tile {
+        Tile t;
+        t.q = min(s.pos / s.per_group, n_groups);
+        t.r = (s.pos - t.q * s.per_group) * s.n;
+        t.n = min(s.n, (t.q < n_groups ? s.wid : s.wid_sh) - t.r);
+        if (t.q < n_groups) {
+            t.first = sm.gfirst[t.q];
+            t.cnt = sm.gfirst[t.q + 1] - t.first;
+            t.expert = sm.gexp[t.q];
         } else {
-            first = 0;
-            cnt = a.m;
-            expert = -1;
+            t.first = 0;
+            t.cnt = a.m;
+            t.expert = -1;
+        }
+        const int inter = t.expert < 0 ? a.inter_sh : a.inter;
+        const size_t e = t.expert < 0 ? 0 : t.expert;
+        if (!down) {
+            const size_t at = (e * inter + t.r) * a.hidden;
+            t.w0 = (t.expert < 0 ? a.S_gate : a.W_gate) + at;
+            t.w1 = (t.expert < 0 ? a.S_up : a.W_up) + at;
+            t.k = a.hidden;
+        } else {
+            t.w0 = (t.expert < 0 ? a.S_down : a.W_down) + (e * a.hidden + h0 + t.r) * inter;
+            t.w1 = nullptr;
+            t.k = inter;
+        }
+        return t;
+    };
+    // The warp's next tile (pos >= end when there is none).
+    const auto next_round = [&](Share& s, bool of_grid) {
+        const int blocks = of_grid ? gridDim.x : 1, b = of_grid ? blockIdx.x : 0;
+        s.round += blocks * kWarps;
+        const int tiles = min(blocks * kWarps, s.end - s.round);
+        if (tiles <= 0) {
+            s.pos = s.end;
+            return;
+        }
+        const int lo = tiles * b / blocks, hi = tiles * (b + 1) / blocks;
+        s.pos = lo + warp < hi ? s.round + lo + warp : s.end;
+    };
+    // Tiles of at most `cap` rows whose rounds over the warps leave the least
+    // of the last one idle.
+    const auto share = [&](int wid, int wid_sh, int cap, bool of_grid) -> Share {
+        Share s;
+        const int workers = of_grid ? gridDim.x * kWarps : kWarps;
+        // lane n - 1 weighs tiles of n rows
+        const int n = lane + 1;
+        const int per = (wid + n - 1) / n, tiles = n_groups * per + (wid_sh + n - 1) / n;
+        const unsigned cost = n <= cap ? static_cast<unsigned>((tiles + workers - 1) / workers * (n + 3)) : UINT_MAX;
+        const unsigned best = __reduce_min_sync(0xffffffffu, cost);
+        const int pick = 31 - __clz(__ballot_sync(0xffffffffu, cost == best));  // the tallest of the best
+        s.n = pick + 1;
+        s.per_group = __shfl_sync(0xffffffffu, per, pick);
+        s.end = __shfl_sync(0xffffffffu, tiles, pick);
+        s.wid = wid;
+        s.wid_sh = wid_sh;
+        s.round = -workers;
+        next_round(s, of_grid);
+        return s;
+    };
+
+    // The producer side of the warp's stream: the tile and column that the
+    // next ring fill takes.
+    const uint32_t ring = smem_u32(&sm.ring[warp][0][0]);
+    Share ps{};
+    Tile pt{};
+    int pk = 0, fill_slot = 0, use_slot = 0;
+    const auto fill = [&](bool down, int h0) {
+        if (ps.pos < ps.end) {
+            const uint32_t slot = ring + fill_slot * kRingBytes;
+            const Tile& t = pt;
+            const bool wide = t.n <= (down ? 16 : 8);
+            const auto row = [&](int r) -> const __nv_bfloat16* {
+                if (down) return r < t.n ? t.w0 + static_cast<size_t>(r) * t.k : nullptr;
+                const int i = (r >> 4) * 8 + (r & 7);  // ring rows: 8 of gate, 8 of up, again
+                return i < t.n ? (r & 8 ? t.w1 : t.w0) + static_cast<size_t>(i) * t.k : nullptr;
+            };
+            if (wide)
+                ring_fill<true>(slot, row, pk, t.k, lane);
+            else
+                ring_fill<false>(slot, row, pk, t.k, lane);
+            pk += wide ? 128 : 64;
+            if (pk >= t.k) {
+                next_round(ps, !(COMBINE && down));
+                pk = 0;
+                if (ps.pos < ps.end) pt = find_tile(down, ps, h0);
+            }
+        }
+        cp_async_commit();  // an empty group once the share is used up, so that waits still count
+        fill_slot = fill_slot + 1 == kStages ? 0 : fill_slot + 1;
+    };
+
+    // Issues the first fills of a share; the fills that the share before it
+    // left over are empty.
+    const auto begin = [&](bool down, const Share& s, int h0) {
+        ps = s;
+        pk = 0;
+        if (ps.pos < ps.end) pt = find_tile(down, ps, h0);
+        use_slot = fill_slot;
+        for (int i = 0; i < kStages - 1; ++i) fill(down, h0);
+    };
+
+    // 32 rows per tile read the tokens half as often; with four token groups
+    // the down phase's three parts leave no registers for it.
+    constexpr int kDownCap = NT == 4 ? 16 : kTileH;
+    float acc[2][NT][4];
+    const __nv_bfloat16* tok[NT];
+    // Runs the warp's share after begin().
+    const auto stream = [&](auto down_tag, Share s, int h0, auto finish) {
+        constexpr bool kDown = decltype(down_tag)::value;
+        constexpr int kParts = kDown ? 3 : 1;
+        for (; s.pos < s.end; next_round(s, !(COMBINE && kDown))) {
+            const Tile t = find_tile(kDown, s, h0);
+            const int nt = (t.cnt + 7) >> 3;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int p = min(n * 8 + g, t.cnt - 1);
+                if (kDown)
+                    tok[n] = (t.expert < 0 ? a.act_sh : a.act) + static_cast<size_t>(t.first + p) * 3 * t.k;
+                else
+                    tok[n] = a.x + static_cast<size_t>(t.expert < 0 ? p : sm.perm[t.first + p] / a.top_k) * t.k;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
+            }
+            const bool wide = t.n <= (kDown ? 16 : 8);
+            for (int k0 = 0; k0 < t.k; k0 += wide ? 128 : 64) {
+                const uint32_t slot = ring + use_slot * kRingBytes;
+                const auto ready = [&] {
+                    cp_async_wait_group<kStages - 2>();
+                    __syncwarp();
+                    // every lane has read the slot of the step before: it is free
+                    fill(kDown, h0);
+                };
+                if (wide || (kDown && kDownCap == 16))
+                    ring_multiply<true, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
+                else
+                    ring_multiply<false, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
+                use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
+            }
+            finish(t, nt);
         }
     };
 
-    // A tile's K steps go round robin over the warps, on from where the last
-    // tile's ended: `rot` is the warp of a tile's first step.  Partial sums are
-    // added from that warp on, so a row's bits depend on K alone and not on
-    // the tiles that came before.
-    int buf = 0, rot = 0;
     // ------------------------------------------------ gate / up -> activation
     {
-        const long long routed = static_cast<long long>(n_groups) * a.inter;
-        const long long total = routed + (n_shared ? a.inter_sh : 0);
-        const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-        const int nkb = (a.hidden + kKb - 1) / kKb;
-        int kb = warp;  // this warp's step of the current tile; steps go round robin over all tiles
-        for (long long pos = lo; pos < hi;) {
-            const int q = pos < routed ? static_cast<int>(pos / a.inter) : n_groups;
-            int first, cnt, expert;
-            group(q, first, cnt, expert);
-            const int width = expert < 0 ? a.inter_sh : a.inter;
-            const int i0 = static_cast<int>(pos - static_cast<long long>(q) * a.inter);
-            int ni = min(kTileI, width - i0);
-            if (ni > hi - pos) ni = static_cast<int>(hi - pos);
-            pos += ni;
-            const size_t row0 = (expert < 0 ? 0 : static_cast<size_t>(expert) * a.inter) + i0;
-            const __nv_bfloat16* wg = (expert < 0 ? a.S_gate : a.W_gate) + row0 * a.hidden;
-            const __nv_bfloat16* wu = (expert < 0 ? a.S_up : a.W_up) + row0 * a.hidden;
-            const int nt = (cnt + 7) >> 3;
-            const __nv_bfloat16* xr[NT];
+        const Share s = share(a.inter, a.inter_sh, kTileI, true);
+        begin(false, s, 0);
+        stream(std::false_type{}, s, 0, [&](const Tile& t, int nt) {
+            // element (h, n, e): gate (e < 2) or up (e >= 2) of row h * 8 + g, token n * 8 + 2 c + e % 2
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int p = min(n * 8 + g, cnt - 1);
-                const int t = expert < 0 ? p : sm.perm[first + p] / a.top_k;
-                xr[n] = a.x + static_cast<size_t>(t) * a.hidden;
-            }
-            float acc[2][NT][4];
+                if (n >= nt) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = h * 8 + g, p = n * 8 + c * 2 + e;
+                        if (row >= t.n || p >= t.cnt) continue;
+                        const float gate = acc[h][n][e];
+                        __nv_bfloat16 part[3];
+                        split_bf16x3(gate / (1.0f + expf(-gate)) * acc[h][n][2 + e], part);
+                        const int width = t.expert < 0 ? a.inter_sh : a.inter;
+                        __nv_bfloat16* dst = (t.expert < 0 ? a.act_sh : a.act) +
+                                             static_cast<size_t>(t.first + p) * 3 * width + t.r + row;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
-            for (; kb < nkb; kb += kWarps) {
-                uint4 wv[2][2][2];  // [32-column piece][row half][gate / up]
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = h * 8 + g;
-                        const bool in = r < ni && k < a.hidden;
-                        wv[s][h][0] = in ? ld_stream_u4(wg + static_cast<size_t>(r) * a.hidden + k) : zero_u4();
-                        wv[s][h][1] = in ? ld_stream_u4(wu + static_cast<size_t>(r) * a.hidden + k) : zero_u4();
+                        for (int z = 0; z < 3; ++z) dst[static_cast<size_t>(z) * width] = part[z];
                     }
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (n >= nt) break;
-                        const uint4 xv = k < a.hidden ? *reinterpret_cast<const uint4*>(xr[n] + k) : zero_u4();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) mma_pieces(acc[h][n], wv[s][h][0], wv[s][h][1], xv);
-                    }
-                }
             }
-            kb -= nkb;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sm.red[buf][warp][(h * NT + n) * 4 + e][lane] = acc[h][n][e];
-            __syncthreads();
-            // element (h, n, e) holds gate (e < 2) or up (e >= 2) of row h * 8 + g, token n * 8 + 2 c + (e & 1)
-            for (int u = tid; u < 2 * NT * 64; u += kThreads) {
-                const int l = u & 31, par = (u >> 5) & 1, hn = u >> 6;
-                const int row = (hn / NT) * 8 + (l >> 2), p = (hn % NT) * 8 + (l & 3) * 2 + par;
-                if (row >= ni || p >= cnt) continue;
-                float gs = 0.0f, us = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    gs += sm.red[buf][(w + rot) % kWarps][hn * 4 + par][l];
-                    us += sm.red[buf][(w + rot) % kWarps][hn * 4 + 2 + par][l];
-                }
-                __nv_bfloat16 part[3];
-                split_bf16x3(gs / (1.0f + expf(-gs)) * us, part);
-                __nv_bfloat16* dst = expert < 0
-                    ? a.act_sh + static_cast<size_t>(p) * 3 * a.inter_sh
-                    : a.act + static_cast<size_t>(first + p) * 3 * a.inter;
-#pragma unroll
-                for (int s = 0; s < 3; ++s) dst[static_cast<size_t>(s) * width + i0 + row] = part[s];
-            }
-            buf ^= 1;
-            rot = (rot + nkb) % kWarps;
-        }
+        });
     }
-    if (!grid_barrier(a.barrier, gridDim.x, &sm.flag, a.status, a.wait_limit_ns)) return;
+
+    // The down weights do not depend on the activation: their first steps are
+    // on their way while the grid meets.
+    grid_arrive(a.barrier);
+    int h0 = h_lo;
+    int nh = COMBINE ? min(kTileH, h_hi - h0) : a.hidden;
+    Share s = share(max(nh, 0), n_shared ? max(nh, 0) : 0, kDownCap, !COMBINE);
+    begin(true, s, h0);
+    if (!grid_wait(a.barrier, gridDim.x, &sm.flag, a.status, a.wait_limit_ns)) return;
 
     // ------------------------------------------------ down + combine
-    const int lo = static_cast<int>(static_cast<long long>(a.hidden) * blockIdx.x / gridDim.x);
-    const int hi = static_cast<int>(static_cast<long long>(a.hidden) * (blockIdx.x + 1) / gridDim.x);
-    int kb = warp;
-    rot = 0;
-    for (int h0 = lo; h0 < hi; h0 += kTileH) {
-        const int nh = min(kTileH, hi - h0);
-        for (int q = 0; q < n_groups + n_shared; ++q) {
-            int first, cnt, expert;
-            group(q, first, cnt, expert);
-            const int width = expert < 0 ? a.inter_sh : a.inter;
-            const int nkb = (width + kKb - 1) / kKb;
-            const __nv_bfloat16* wd =
-                expert < 0 ? a.S_down + static_cast<size_t>(h0) * width
-                           : a.W_down + (static_cast<size_t>(expert) * a.hidden + h0) * width;
-            const __nv_bfloat16* act = expert < 0 ? a.act_sh : a.act;
-            const int nt = (cnt + 7) >> 3;
-            float acc[2][NT][4];
+    // element (h, n, e): hidden row h * 16 + (e / 2) * 8 + g, token n * 8 + 2 c + e % 2
+    const auto each_output = [&](const Tile& t, int nt, auto store) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n >= nt) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
-            for (; kb < nkb; kb += kWarps) {
-                uint4 wv[2][4];  // [32-column piece][group of 8 rows]
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const int r = h * 8 + g;
-                        wv[s][h] = r < nh && k < width ? ld_stream_u4(wd + static_cast<size_t>(r) * width + k)
-                                                       : zero_u4();
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int row = h * 16 + (e >> 1) * 8 + g, p = n * 8 + c * 2 + (e & 1);
+                    if (row < t.n && p < t.cnt)
+                        store(t.expert < 0 ? rows + p : sm.perm[t.first + p], t.r + row, acc[h][n][e]);
                 }
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (n >= nt) break;
-                        const __nv_bfloat16* ar =
-                            act + static_cast<size_t>(first + min(n * 8 + g, cnt - 1)) * 3 * width + k;
-#pragma unroll
-                        for (int z = 2; z >= 0; --z) {
-                            const uint4 av = k < width
-                                ? *reinterpret_cast<const uint4*>(ar + static_cast<size_t>(z) * width)
-                                : zero_u4();
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                mma_pieces(acc[h][n], wv[s][2 * h], wv[s][2 * h + 1], av);
-                        }
-                    }
-                }
-            }
-            kb -= nkb;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sm.red[buf][warp][(h * NT + n) * 4 + e][lane] = acc[h][n][e];
+        }
+    };
+    if (COMBINE) {
+        while (h0 < h_hi) {
+            stream(std::true_type{}, s, h0, [&](const Tile& t, int nt) {
+                each_output(t, nt, [&](int r, int h, float v) { sm_d[r][h] = v; });
+            });
             __syncthreads();
-            // element (h, n, e): hidden row h * 16 + (e / 2) * 8 + g, token n * 8 + 2 c + (e & 1)
-            for (int u = tid; u < 2 * NT * 4 * 32; u += kThreads) {
-                const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) % NT, h = (hne >> 2) / NT;
-                const int p = n * 8 + (l & 3) * 2 + (e & 1);
-                if (p >= cnt) continue;
-                float s = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += sm.red[buf][(w + rot) % kWarps][hne][l];
-                sm.d[expert < 0 ? rows + p : sm.perm[first + p]][h * 16 + (e >> 1) * 8 + (l >> 2)] = s;
+            for (int u = tid; u < a.m * kTileH; u += kThreads) {
+                const int t = u / kTileH, h = u % kTileH;
+                if (h >= nh) continue;
+                float y = 0.0f;
+                for (int j = 0; j < a.top_k; ++j) y += sm.weight[t * a.top_k + j] * sm_d[t * a.top_k + j][h];
+                if (n_shared) y += a.gate[t] * sm_d[rows + t][h];
+                a.y[static_cast<size_t>(t) * a.hidden + h0 + h] = y;
             }
-            buf ^= 1;
-            rot = (rot + nkb) % kWarps;
+            __syncthreads();
+            h0 += kTileH;
+            nh = min(kTileH, h_hi - h0);
+            if (h0 >= h_hi) break;
+            s = share(nh, n_shared ? nh : 0, kDownCap, false);
+            begin(true, s, h0);
         }
-        __syncthreads();
-        for (int u = tid; u < a.m * kTileH; u += kThreads) {
-            const int t = u / kTileH, h = u % kTileH;
-            if (h >= nh) continue;
-            float y = 0.0f;
-            for (int j = 0; j < a.top_k; ++j) {
-                const int r = t * a.top_k + j;
-                y += sm.weight[r] * sm.d[r][h];
-            }
-            if (n_shared) y += a.gate[t] * sm.d[rows + t][h];
-            a.y[static_cast<size_t>(t) * a.hidden + h0 + h] = y;
+    } else {
+        stream(std::true_type{}, s, 0, [&](const Tile& t, int nt) {
+            each_output(t, nt, [&](int r, int h, float v) { a.d[static_cast<size_t>(r) * a.hidden + h] = v; });
+        });
+        grid_arrive(a.barrier);
+        if (!grid_wait(a.barrier, 2 * gridDim.x, &sm.flag, a.status, a.wait_limit_ns)) return;
+        const int total = a.m * (a.hidden / 4);
+        for (int u = blockIdx.x * kThreads + tid; u < total; u += gridDim.x * kThreads) {
+            const int t = u / (a.hidden / 4), h = (u % (a.hidden / 4)) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            const auto add = [&](float w, size_t r) {
+                const float4 v = *reinterpret_cast<const float4*>(a.d + r * a.hidden + h);
+                y.x += w * v.x;
+                y.y += w * v.y;
+                y.z += w * v.z;
+                y.w += w * v.w;
+            };
+            for (int j = 0; j < a.top_k; ++j) add(sm.weight[t * a.top_k + j], t * a.top_k + j);
+            if (n_shared) add(a.gate[t], rows + t);
+            *reinterpret_cast<float4*>(a.y + static_cast<size_t>(t) * a.hidden + h) = y;
         }
-        __syncthreads();
     }
 }
 
-template <int NT>
+template <int NT, bool COMBINE>
 cudaError_t launch_experts(const LayerDecodeArgs& args, int num_sms, cudaStream_t stream) {
-    // the routing keys of the min(16, 8 NT) warps that route lie in the partial-sum buffers
-    static_assert(sizeof(ExpertsSmem<NT>::red) >= sizeof(float) * MOE_MAX_EXPERTS * (NT < 2 ? 8 : kWarps),
-                  "routing scratch");
-    constexpr int smem = sizeof(ExpertsSmem<NT>);
+    const int d_rows = COMBINE ? args.m * (args.top_k + (args.inter_sh > 0 ? 1 : 0)) : 0;
+    const int smem = static_cast<int>(sizeof(ExpertsSmem)) + d_rows * (kTileH + 1) * 4;
     static PerDeviceOnce once;
     cudaError_t err = once.run([] {
-        return cudaFuncSetAttribute(layer_experts_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(layer_experts_kernel<NT, COMBINE>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
     });
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
@@ -440,12 +576,14 @@ cudaError_t launch_experts(const LayerDecodeArgs& args, int num_sms, cudaStream_
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, layer_experts_kernel<NT>, args);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, layer_experts_kernel<NT, COMBINE>, args);
 }
 
 }  // namespace
@@ -459,9 +597,11 @@ cudaError_t launch_layer_decode(const LayerDecodeArgs& args, const __nv_bfloat16
         const_cast<float*>(args.scores), const_cast<float*>(args.gate), args.barrier, args.status);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    if (args.m <= 8) return launch_experts<1>(args, num_sms, stream);
-    if (args.m <= 16) return launch_experts<2>(args, num_sms, stream);
-    return launch_experts<4>(args, num_sms, stream);
+    const int d_rows = args.m * (args.top_k + (args.inter_sh > 0 ? 1 : 0));
+    if (args.m <= 8 && d_rows <= kCombineRows) return launch_experts<1, true>(args, num_sms, stream);
+    if (args.m <= 8) return launch_experts<1, false>(args, num_sms, stream);
+    if (args.m <= 16) return launch_experts<2, false>(args, num_sms, stream);
+    return launch_experts<4, false>(args, num_sms, stream);
 }
 
 }  // namespace moe
