@@ -915,31 +915,61 @@ MOE_API moe_status_t moe_layer_decode(
 
 namespace {
 
-// K ranges of the adapters' first product: enough blocks (32 tokens x 32
-// adapter rows x one range each) to occupy the SMs, at least two steps of a
-// block's 16 warps per range.  A function of the shape alone.
+// K ranges of the adapters' first product on the streaming path: enough blocks
+// (up to 32 adapters of 32 tokens x 32 adapter rows x one range each) to
+// occupy the SMs, at least two steps of a block's 16 warps per range.  A
+// function of the shape alone.
 int lora_k_splits(long long m, int k, int rank) {
-    const long long blocks = ((m + 31) / 32) * ((rank + 31) / 32);
+    if (m > moe::kLoraStreamMaxTokens) return 1;
+    const long long blocks = (m < 32 ? m : (m + 31) / 32 * 32) * ((rank + 31) / 32);
     const long long by_sms = blocks > 0 ? 148 / blocks : 1;
     const long long by_k = k / 2048;
     const long long s = by_sms < by_k ? by_sms : by_k;
     return s < 1 ? 1 : s > 8 ? 8 : static_cast<int>(s);
 }
 
-// Status word, the partial sums h [k_splits, m, rank], and for the larger
-// batches the projection [m, n] f32 before the adapters' part is added.
+// Columns of a GEMM tile (a multiple of 32, at most 256): the width whose
+// tiles (256 tokens high, one per CTA pair at a time) take the least time.  A
+// stage of 64 columns of K costs the larger of its MMAs (2 cycles per column)
+// and its copies (16 KB + 64 bytes per column and CTA, at about 80 bytes a
+// cycle).
+int lora_tile_columns(long long m, int n) {
+    int pick = 256;
+    double best = 0;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const long long tiles = (m + 255) / 256 * ((n + bn - 1) / bn);
+        const double stage = 2.0 * bn > 205 + 0.8 * bn ? 2.0 * bn : 205 + 0.8 * bn;
+        const double cost = static_cast<double>((tiles + 73) / 74) * stage;
+        if (bn == 256 || cost < best) {
+            best = cost;
+            pick = bn;
+        }
+    }
+    return pick;
+}
+
+// Status word, then the adapters' first products: on the streaming path the
+// partial sums h [k_splits, m, rank], for the GEMM the two bf16 parts
+// [m, 2, r16] and the adapters of each row tile.
 struct LoraLayout {
-    size_t status, h, base, end;
-    int k_splits;
+    size_t status, h, count, list, end;
+    int k_splits, r16;
 };
 
-LoraLayout lora_layout(long long m, int n, int k, int rank) {
+LoraLayout lora_layout(long long m, int k, int rank) {
     Carver c;
-    LoraLayout L;
+    LoraLayout L{};
     L.k_splits = lora_k_splits(m, k, rank);
+    L.r16 = (rank + 15) / 16 * 16;
     L.status = c.take(sizeof(int));
-    L.h = c.take(sizeof(float) * L.k_splits * static_cast<size_t>(m) * rank);
-    L.base = c.take(m > moe::kLoraStreamMaxTokens ? sizeof(float) * static_cast<size_t>(m) * n : 0);
+    if (m <= moe::kLoraStreamMaxTokens) {
+        L.h = c.take(sizeof(float) * L.k_splits * static_cast<size_t>(m) * rank);
+    } else {
+        const size_t tiles = static_cast<size_t>((m + moe::kLoraTileRows - 1) / moe::kLoraTileRows);
+        L.h = c.take(sizeof(uint16_t) * 2 * static_cast<size_t>(m) * L.r16);
+        L.count = c.take(sizeof(int) * tiles);
+        L.list = c.take(sizeof(int) * tiles * moe::kLoraTileRows);
+    }
     L.end = c.off;
     return L;
 }
@@ -967,7 +997,7 @@ extern "C" {
 MOE_API size_t moe_matmul_lora_workspace(int32_t m, int32_t n, int32_t k, int32_t rank,
                                          int32_t n_adapters) {
     if (check_lora_shape(m, n, k, rank, n_adapters) != MOE_OK) return 0;
-    return lora_layout(m, n, k, rank).end;
+    return lora_layout(m, k, rank).end;
 }
 
 MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
@@ -987,7 +1017,7 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     MOE_TRY(check_ptr(B, "B", 16));
     if (scales) MOE_TRY(check_ptr(scales, "scales", 4));
     MOE_TRY(check_ptr(y, "y", 16));
-    const LoraLayout L = lora_layout(m, n, k, rank);
+    const LoraLayout L = lora_layout(m, k, rank);
     MOE_TRY(check_ws(ws, ws_bytes, L.end));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* wsb = static_cast<char*>(ws);
@@ -999,7 +1029,14 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.A = bf(A);
     a.B = bf(B);
     a.scales = scales;
-    a.h = reinterpret_cast<float*>(wsb + L.h);
+    const bool stream_w = m <= moe::kLoraStreamMaxTokens;
+    if (stream_w) {
+        a.h = reinterpret_cast<float*>(wsb + L.h);
+    } else {
+        a.h_split = reinterpret_cast<__nv_bfloat16*>(wsb + L.h);
+        a.tile_count = reinterpret_cast<int*>(wsb + L.count);
+        a.tile_list = reinterpret_cast<int*>(wsb + L.list);
+    }
     a.y = y;
     a.status = reinterpret_cast<int*>(wsb + L.status);
     a.m = m;
@@ -1009,32 +1046,19 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.n_adapters = n_adapters;
     a.k_splits = L.k_splits;
     a.y_dtype = y_dtype;
+    a.r16 = L.r16;
+    a.wait_limit_ns = moe::kDefaultWaitLimitNs;
+    const int bn = stream_w ? 0 : lora_tile_columns(m, n);
+    CUtensorMap map_x, map_w;
+    if (!stream_w) {
+        MOE_TRY(make_map(&map_x, x, k, m, 128, "x"));
+        MOE_TRY(make_map(&map_w, W, k, n, bn / 2, "W"));
+    }
     cudaError_t err = moe::launch_lora_shrink(a, s);
     if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
-    if (m <= moe::kLoraStreamMaxTokens) {
-        err = moe::launch_lora_stream(a, num_sms(), s);
-        if (err != cudaSuccess) return cuda_fail(err, "streaming projection launch");
-        return ok();
-    }
-    CUtensorMap map_x, map_w;
-    MOE_TRY(make_map(&map_x, x, k, m, 128, "x"));
-    MOE_TRY(make_map(&map_w, W, k, n, 256, "W"));
-    float* base = reinterpret_cast<float*>(wsb + L.base);
-    moe::GroupedGemmArgs g{};
-    g.out = base;
-    g.status = a.status;
-    g.status_out = a.status;
-    g.rows = m;
-    g.n = n;
-    g.k = k;
-    g.n_col_tiles = (n + 255) / 256;
-    g.dense_m_tiles = (m + moe::kTileRows - 1) / moe::kTileRows;
-    g.k_splits = 1;
-    g.wait_limit_ns = moe::kDefaultWaitLimitNs;
-    err = moe::launch_grouped_gemm(4, map_x, map_w, map_w, g, num_sms(), s);
+    err = stream_w ? moe::launch_lora_stream(a, num_sms(), s)
+                   : moe::launch_lora_gemm(a, map_x, map_w, bn, num_sms(), s);
     if (err != cudaSuccess) return cuda_fail(err, "projection launch");
-    err = moe::launch_lora_add(a, base, num_sms(), s);
-    if (err != cudaSuccess) return cuda_fail(err, "adapter launch");
     return ok();
 }
 

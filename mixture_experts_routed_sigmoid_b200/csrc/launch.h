@@ -200,7 +200,8 @@ cudaError_t launch_layer_decode(const LayerDecodeArgs& args, const __nv_bfloat16
                                 cudaStream_t stream);
 
 // Shared projection with per-token low-rank adapters.
-constexpr int kLoraStreamMaxTokens = 64;
+constexpr int kLoraStreamMaxTokens = 64;  // m up to which W is streamed
+constexpr int kLoraTileRows = 256;        // tokens of a GEMM tile
 struct LoraArgs {
     const __nv_bfloat16* x;  // [m, k]
     const __nv_bfloat16* W;  // [n, k]
@@ -208,15 +209,21 @@ struct LoraArgs {
     const __nv_bfloat16* A;  // [n_adapters, rank, k]
     const __nv_bfloat16* B;  // [n_adapters, n, rank]
     const float* scales;     // [n_adapters] or null
-    float* h;                // [k_splits, m, rank] partial sums of A x
+    float* h;                // streamed: [k_splits, m, rank] partial sums of A x
+    __nv_bfloat16* h_split;  // GEMM: [m, 2, r16] scales * A x as two bf16 parts
+    int* tile_count;         // GEMM: adapters that occur in each tile's tokens
+    int* tile_list;          // GEMM: [tiles, kLoraTileRows] those adapters
     void* y;                 // [m, n]
     int* status;
     long long m;
-    int n, k, rank, n_adapters, k_splits, y_dtype;
+    int n, k, rank, r16, n_adapters, k_splits, y_dtype;
+    unsigned long long wait_limit_ns;
 };
 cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream);
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_lora_add(const LoraArgs& a, const float* base, int num_sms, cudaStream_t stream);
+// map_x: boxes of 128 rows, map_w: boxes of bn / 2 rows (64 columns each).
+cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
+                             int num_sms, cudaStream_t stream);
 
 // Sets the calling thread's moe_last_error() message.
 void set_last_error(const char* msg);

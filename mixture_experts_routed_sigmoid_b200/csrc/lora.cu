@@ -10,7 +10,7 @@
 //   that holds NaN or infinities reaches its own requests only.
 // Kernel 2, m <= 64: streams W once through mma.sync (stream_mma.cuh) and
 //   adds scales[a] * B[a] h in its epilogue.
-// Kernel 2 and 3, larger m: the tcgen05 projection, then the adapters' part.
+// Kernel 2, larger m: the tcgen05 GEMM of lora_gemm.cu.
 #include "launch.h"
 #include "stream_mma.cuh"
 
@@ -25,13 +25,20 @@ constexpr int kRankTile = 32; // adapter rows per shrink block
 constexpr int kTileN = 32;    // output columns of a streaming tile
 
 // ------------------------------------------------------------------ shrink
-// grid: (token groups, rank tiles, K ranges).  K range z writes its partial
-// sums to h + z * m * rank; the reader adds the ranges in order.
-__global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs a) {
+// grid: (token groups, rank tiles x adapter lanes, K ranges).  Adapter lane j
+// of L takes every L-th adapter of its tokens.  The streaming kernel gets the
+// f32 sums, K range z at h + z * m * rank (it adds the ranges in order); the
+// GEMM gets them scaled and split into two bf16 parts, with the list of the
+// adapters that occur in each of its row tiles.
+template <bool GEMM>
+__global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs a, int rank_tiles) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     float(*red)[2 * 4 * 4][32] = reinterpret_cast<float(*)[2 * 4 * 4][32]>(smem_raw);  // [kWarps]
-    __shared__ int s_id[kGroup];
+    __shared__ __align__(16) int s_id[kGroup];
+    __shared__ __align__(16) int s_tile[kLoraTileRows];
+    __shared__ int s_count[kLoraTileRows / 32];
     __shared__ int s_bad;
+    allow_next_kernel();  // it waits for this one's writes before it reads them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c8 = (lane & 3) * 8;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
@@ -47,6 +54,41 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs
         __syncthreads();
         if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
     }
+    if (GEMM && blockIdx.y == 0 && blockIdx.x % (kLoraTileRows / kGroup) == 0) {
+        // the adapters of this block's row tile, in order of their first token
+        const long long first = static_cast<long long>(blockIdx.x) * kGroup;
+        int id = -1;
+        if (tid < kLoraTileRows) {
+            if (first + tid < a.m) id = a.adapter_ids[first + tid];
+            if (id >= a.n_adapters) id = -1;
+            s_tile[tid] = id;
+        }
+        __syncthreads();
+        bool opens = false;
+        unsigned ballot = 0;
+        if (tid < kLoraTileRows) {
+            const unsigned twins = __match_any_sync(0xffffffffu, id);  // every lane takes part
+            opens = id >= 0 && __ffs(twins) - 1 == lane;
+            for (int j = 0; j < warp * 8; ++j) {
+                const int4 v = reinterpret_cast<const int4*>(s_tile)[j];
+                opens = opens && v.x != id && v.y != id && v.z != id && v.w != id;
+            }
+            ballot = __ballot_sync(0xffffffffu, opens);
+            if (lane == 0) s_count[warp] = __popc(ballot);
+        }
+        __syncthreads();
+        const int mt = static_cast<int>(first / kLoraTileRows);
+        if (tid < kLoraTileRows) {
+            int before = 0, total = 0;
+            for (int w = 0; w < kLoraTileRows / 32; ++w) {
+                if (w < warp) before += s_count[w];
+                total += s_count[w];
+            }
+            if (opens)
+                a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + before + __popc(ballot & lanemask_lt())] = id;
+            if (tid == 0) a.tile_count[mt] = total;
+        }
+    }
     const long long t0 = static_cast<long long>(blockIdx.x) * kGroup;
     const int nt_here = static_cast<int>(min(static_cast<long long>(kGroup), a.m - t0));
     if (tid < kGroup) {
@@ -59,15 +101,17 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs
     // lanes that open an adapter: the first token of each distinct id
     const unsigned same = __match_any_sync(0xffffffffu, my_id);
     unsigned leaders = __ballot_sync(0xffffffffu, my_id >= 0 && (__ffs(same) - 1) == lane);
-    const int r0 = blockIdx.y * kRankTile;
+    const int adapter_lanes = gridDim.y / rank_tiles, my_lane = blockIdx.y / rank_tiles;
+    const int r0 = static_cast<int>(blockIdx.y % rank_tiles) * kRankTile;
     const int nr = min(kRankTile, a.rank - r0);
     const int nkb_all = (a.k + kKb - 1) / kKb;
     const int kb_lo = static_cast<int>(static_cast<long long>(nkb_all) * blockIdx.z / gridDim.z);
     const int kb_hi = static_cast<int>(static_cast<long long>(nkb_all) * (blockIdx.z + 1) / gridDim.z);
     float* h_out = a.h + static_cast<size_t>(blockIdx.z) * a.m * a.rank;
-    while (leaders) {
+    for (int j = 0; leaders; ++j) {
         const int lead = __ffs(leaders) - 1;
         leaders &= leaders - 1;
+        if (j % adapter_lanes != my_lane) continue;
         const int ad = s_id[lead];
         const unsigned mine = __ballot_sync(0xffffffffu, my_id == ad);  // tokens of this adapter
         const __nv_bfloat16* A = a.A + (static_cast<size_t>(ad) * a.rank + r0) * a.k;
@@ -113,11 +157,22 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs
         for (int u = tid; u < 2 * 4 * 4 * 32; u += kThreads) {
             const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) & 3, h = hne >> 4;
             const int p = n * 8 + (l & 3) * 2 + (e & 1), r = h * 16 + (e >> 1) * 8 + (l >> 2);
-            if (!(mine >> p & 1u) || r >= nr) continue;
+            if (!(mine >> p & 1u) || (GEMM ? r0 + r >= a.r16 : r >= nr)) continue;
             float s = 0.0f;
+            if (r < nr) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[w][hne][l];
-            h_out[(t0 + p) * a.rank + r0 + r] = s;
+                for (int w = 0; w < kWarps; ++w) s += red[w][hne][l];
+            }
+            if (GEMM) {
+                if (a.scales) s *= a.scales[ad];
+                __nv_bfloat16 part[3];
+                split_bf16x3(s, part);
+                __nv_bfloat16* dst = a.h_split + static_cast<size_t>(t0 + p) * 2 * a.r16 + r0 + r;
+                dst[0] = part[0];
+                dst[a.r16] = part[1];
+            } else {
+                h_out[(t0 + p) * a.rank + r0 + r] = s;
+            }
         }
         __syncthreads();
     }
@@ -246,26 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) lora_stream_kernel(const LoraArgs
     }
 }
 
-// --------------------------------------------------------- adding (larger m)
-__global__ void __launch_bounds__(256) lora_add_kernel(const LoraArgs a, const float* __restrict__ base) {
-    if (*a.status != kDevOk) return;
-    const long long total = a.m * a.n;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += static_cast<long long>(gridDim.x) * 256) {
-        const long long t = i / a.n;
-        const int c = static_cast<int>(i - t * a.n);
-        const int id = a.adapter_ids[t];
-        float v = base[i];
-        if (id >= 0) {
-            float s = 0.0f;
-            const __nv_bfloat16* b = a.B + (static_cast<size_t>(id) * a.n + c) * a.rank;
-            for (int z = 0; z < a.k_splits; ++z)
-                s += expand_dot(b, a.h + (static_cast<size_t>(z) * a.m + t) * a.rank, a.rank);
-            v += (a.scales ? a.scales[id] : 1.0f) * s;
-        }
-        store_y(a.y, a.y_dtype, i, v);
-    }
-}
-
 template <int NT>
 cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     static PerDeviceOnce once;
@@ -280,17 +315,28 @@ cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
+template <bool GEMM>
+static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
     static PerDeviceOnce once;
     constexpr int smem = kWarps * 2 * 4 * 4 * 32 * sizeof(float);
     cudaError_t err = once.run([] {
-        return cudaFuncSetAttribute(lora_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(lora_shrink_kernel<GEMM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err != cudaSuccess) return err;
-    const dim3 grid(static_cast<unsigned>((a.m + kGroup - 1) / kGroup), (a.rank + kRankTile - 1) / kRankTile,
-                    a.k_splits);
-    lora_shrink_kernel<<<grid, kThreads, smem, stream>>>(a);
+    const unsigned groups = static_cast<unsigned>((a.m + kGroup - 1) / kGroup);
+    const unsigned rank_tiles = (a.rank + kRankTile - 1) / kRankTile;
+    // a block per adapter for a few tokens, one for all of them when the
+    // token groups fill the SMs by themselves
+    const unsigned most = static_cast<unsigned>(a.m < kGroup ? a.m : kGroup);
+    unsigned lanes = 296 / (groups * rank_tiles * a.k_splits);
+    lanes = lanes < 1 ? 1 : lanes > most ? most : lanes;
+    lora_shrink_kernel<GEMM><<<dim3(groups, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
+        a, static_cast<int>(rank_tiles));
     return cudaGetLastError();
+}
+
+cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
+    return a.h_split ? launch_shrink<true>(a, stream) : launch_shrink<false>(a, stream);
 }
 
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
@@ -298,11 +344,6 @@ cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stre
     if (a.m <= 16) return launch_stream<2>(a, num_sms, stream);
     if (a.m <= 32) return launch_stream<4>(a, num_sms, stream);
     return launch_stream<8>(a, num_sms, stream);
-}
-
-cudaError_t launch_lora_add(const LoraArgs& a, const float* base, int num_sms, cudaStream_t stream) {
-    lora_add_kernel<<<num_sms * 8, 256, 0, stream>>>(a, base);
-    return cudaGetLastError();
 }
 
 }  // namespace moe

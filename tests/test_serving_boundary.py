@@ -53,8 +53,8 @@ def test_layer_decode_validation(lib):
 
 def test_layer_decode_workspace(lib):
     f = lib.moe_layer_decode_workspace
-    # the activation as three bf16 parts, the scores
-    fixed = 3 * 2 * (16 * 8 * 768 + 16 * 512) + 4 * 16 * 128
+    # the activation as three bf16 parts, the scores, the down outputs of every slot
+    fixed = 3 * 2 * (16 * 8 * 768 + 16 * 512) + 4 * 16 * 128 + 4 * 16 * 9 * 2048
     assert fixed <= f(16, 2048, 768, 512, 8, 128) < fixed + 4096
     assert f(33, 64, 32, 0, 1, 8) == 0 and f(4, 60, 32, 0, 2, 8) == 0 and f(4, 64, 32, 4, 2, 8) == 0
     assert f(0, 64, 32, 0, 2, 8) > 0
