@@ -3,11 +3,13 @@
 //   y[t] = W x[t] + scales[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
 // (a = -1: the projection alone).
 //
-// Kernel 1 (shrink): h[t] = A[a] x[t], f32 [m, rank].  A block takes 32
-//   consecutive tokens and walks the adapters that occur among them; the
-//   tokens of another adapter ride along in the MMA's unused columns and are
-//   dropped by selection, never by a multiplication with zero, so an adapter
-//   that holds NaN or infinities reaches its own requests only.
+// Kernel 1 (shrink): h[t] = A[a] x[t].  An item is 32 consecutive tokens and
+//   one of the adapters that occur among them; only those tokens' rows of x
+//   are read.  The tokens are the rows of the MMA (stream_mma.cuh, with x in
+//   the place of the weights), the adapter's rank its columns; rows of other
+//   tokens are dropped by selection, never by a multiplication with zero, so
+//   an adapter that holds NaN or infinities reaches its own requests only.
+//   It reads x once from HBM, where the projection then finds it in the L2.
 // Kernel 2, m <= 64: streams W once through mma.sync (stream_mma.cuh) and
 //   adds scales[a] * B[a] h in its epilogue.
 // Kernel 2, larger m: the tcgen05 GEMM of lora_gemm.cu.
@@ -20,32 +22,38 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKb = 64;       // K columns of one warp step
-constexpr int kGroup = 32;    // tokens per shrink block
-constexpr int kRankTile = 32; // adapter rows per shrink block
+constexpr int kGroup = 32;    // tokens of a shrink item
 constexpr int kTileN = 32;    // output columns of a streaming tile
 
 // ------------------------------------------------------------------ shrink
-// grid: (token groups, rank tiles x adapter lanes, K ranges).  Adapter lane j
-// of L takes every L-th adapter of its tokens.  The streaming kernel gets the
-// f32 sums, K range z at h + z * m * rank (it adds the ranges in order); the
-// GEMM gets them scaled and split into two bf16 parts, with the list of the
-// adapters that occur in each of its row tiles.
-template <bool GEMM>
-__global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs a, int rank_tiles) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    float(*red)[2 * 4 * 4][32] = reinterpret_cast<float(*)[2 * 4 * 4][32]>(smem_raw);  // [kWarps]
-    __shared__ __align__(16) int s_id[kGroup];
+// grid: (token groups / groups per block, rank tiles x adapter lanes, K
+// ranges).  `ks` warps split the K of an item; a block holds 16 / ks token
+// groups.  Adapter lane j of L takes every L-th adapter of its tokens.  The
+// streaming kernel gets the f32 sums, K range z at h + z * m * rank (it adds
+// the ranges in order); the GEMM gets them scaled and split into two bf16
+// parts, with the list of the adapters that occur in each of its row tiles.
+constexpr int kShrinkStages = 3;
+
+__device__ __forceinline__ void item_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+template <bool GEMM, int NT>  // NT: groups of 8 rank rows per item
+__global__ void __launch_bounds__(kThreads, 1)
+    lora_shrink_kernel(const LoraArgs a, int rank_tiles, int ks) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
     __shared__ __align__(16) int s_tile[kLoraTileRows];
     __shared__ int s_count[kLoraTileRows / 32];
     __shared__ int s_bad;
     allow_next_kernel();  // it waits for this one's writes before it reads them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c8 = (lane & 3) * 8;
+    const int g = lane >> 2;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
         // the call's status word: any adapter id outside [-1, n_adapters)
         if (tid == 0) s_bad = 0;
         __syncthreads();
         bool bad = false;
+#pragma unroll 8
         for (long long t = tid; t < a.m; t += kThreads) {
             const int id = a.adapter_ids[t];
             bad |= id < -1 || id >= a.n_adapters;
@@ -54,9 +62,10 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs
         __syncthreads();
         if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
     }
-    if (GEMM && blockIdx.y == 0 && blockIdx.x % (kLoraTileRows / kGroup) == 0) {
-        // the adapters of this block's row tile, in order of their first token
-        const long long first = static_cast<long long>(blockIdx.x) * kGroup;
+    const int block_tokens = kWarps / ks * kGroup;  // 32 to 256
+    const long long first = static_cast<long long>(blockIdx.x) * block_tokens;
+    if (GEMM && blockIdx.y == 0 && first % kLoraTileRows == 0) {
+        // the adapters of the row tile that begins here, in order of their first token
         int id = -1;
         if (tid < kLoraTileRows) {
             if (first + tid < a.m) id = a.adapter_ids[first + tid];
@@ -89,92 +98,94 @@ __global__ void __launch_bounds__(kThreads, 1) lora_shrink_kernel(const LoraArgs
             if (tid == 0) a.tile_count[mt] = total;
         }
     }
-    const long long t0 = static_cast<long long>(blockIdx.x) * kGroup;
-    const int nt_here = static_cast<int>(min(static_cast<long long>(kGroup), a.m - t0));
-    if (tid < kGroup) {
-        int id = tid < nt_here ? a.adapter_ids[t0 + tid] : -1;
-        if (id >= a.n_adapters) id = -1;  // reported above; no adapter is read for it
-        s_id[tid] = id;
-    }
-    __syncthreads();
-    const int my_id = s_id[lane];
+    const int item = warp / ks, part = warp % ks;  // this warp's tokens and its share of K
+    const long long t0 = first + item * kGroup;
+    int my_id = t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
+    if (my_id >= a.n_adapters) my_id = -1;  // reported above; no adapter is read for it
     // lanes that open an adapter: the first token of each distinct id
     const unsigned same = __match_any_sync(0xffffffffu, my_id);
     unsigned leaders = __ballot_sync(0xffffffffu, my_id >= 0 && (__ffs(same) - 1) == lane);
     const int adapter_lanes = gridDim.y / rank_tiles, my_lane = blockIdx.y / rank_tiles;
-    const int r0 = static_cast<int>(blockIdx.y % rank_tiles) * kRankTile;
-    const int nr = min(kRankTile, a.rank - r0);
-    const int nkb_all = (a.k + kKb - 1) / kKb;
-    const int kb_lo = static_cast<int>(static_cast<long long>(nkb_all) * blockIdx.z / gridDim.z);
-    const int kb_hi = static_cast<int>(static_cast<long long>(nkb_all) * (blockIdx.z + 1) / gridDim.z);
-    float* h_out = a.h + static_cast<size_t>(blockIdx.z) * a.m * a.rank;
+    const int r0 = static_cast<int>(blockIdx.y % rank_tiles) * NT * 8;
+    const int nr = min(NT * 8, a.rank - r0), nt = (nr + 7) >> 3;
+    const int nkb = (a.k + kKb - 1) / kKb, shares = ks * gridDim.z, share = blockIdx.z * ks + part;
+    const int k_lo = static_cast<int>(static_cast<long long>(nkb) * share / shares) * kKb;
+    const int k_hi = min(a.k, static_cast<int>(static_cast<long long>(nkb) * (share + 1) / shares) * kKb);
+    unsigned char* ring_mem = smem_raw + warp * kShrinkStages * kRingBytes;
+    const uint32_t ring = smem_u32(ring_mem);
+    static_assert(kShrinkStages * kRingBytes >= 2 * NT * 4 * 32 * 4, "partial sums lie in the ring");
     for (int j = 0; leaders; ++j) {
         const int lead = __ffs(leaders) - 1;
         leaders &= leaders - 1;
         if (j % adapter_lanes != my_lane) continue;
-        const int ad = s_id[lead];
+        const int ad = __shfl_sync(0xffffffffu, my_id, lead);
         const unsigned mine = __ballot_sync(0xffffffffu, my_id == ad);  // tokens of this adapter
+        const float scale = GEMM && a.scales ? a.scales[ad] : 1.0f;
         const __nv_bfloat16* A = a.A + (static_cast<size_t>(ad) * a.rank + r0) * a.k;
-        float acc[2][4][4];
+        const __nv_bfloat16* tok[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) tok[n] = A + static_cast<size_t>(min(n * 8 + g, nr - 1)) * a.k;
+        float acc[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
-        for (int kb = kb_lo + warp; kb < kb_hi; kb += kWarps) {
-            uint4 wv[2][4];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int r = h * 8 + g;
-                    wv[s][h] = r < nr && k < a.k
-                        ? *reinterpret_cast<const uint4*>(A + static_cast<size_t>(r) * a.k + k) : zero_u4();
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    if (!(mine >> (8 * n) & 0xffu)) continue;  // warp-uniform
-                    const long long t = t0 + min(n * 8 + g, nt_here - 1);
-                    const uint4 xv = k < a.k ? *reinterpret_cast<const uint4*>(a.x + t * a.k + k) : zero_u4();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) mma_pieces(acc[h][n], wv[s][2 * h], wv[s][2 * h + 1], xv);
-                }
-            }
+        const auto row = [&](int r) -> const __nv_bfloat16* {
+            return mine >> r & 1u ? a.x + (t0 + r) * a.k : nullptr;
+        };
+        int fill_k = k_lo, fill_slot = 0, use_slot = 0;
+        const auto fill = [&] {
+            if (fill_k < k_hi) ring_fill<false>(ring + fill_slot * kRingBytes, row, fill_k, a.k, lane);
+            fill_k += kKb;
+            cp_async_commit();
+            fill_slot = fill_slot + 1 == kShrinkStages ? 0 : fill_slot + 1;
+        };
+        for (int i = 0; i < kShrinkStages - 1; ++i) fill();
+        for (int k0 = k_lo; k0 < k_hi; k0 += kKb) {
+            const uint32_t slot = ring + use_slot * kRingBytes;
+            ring_multiply<false, NT, 1>(acc, slot, tok, nt, k0, a.k, lane, [&] {
+                cp_async_wait_group<kShrinkStages - 2>();
+                __syncwarp();
+                fill();
+            });
+            use_slot = use_slot + 1 == kShrinkStages ? 0 : use_slot + 1;
         }
+        // element (h, n, e): token h * 16 + (e / 2) * 8 + g, rank row n * 8 + 2 c + e % 2
+        const auto finish = [&](int token, int r, float v) {
+            if (!(mine >> token & 1u) || (GEMM ? r0 + r >= a.r16 : r >= nr)) return;
+            if (r >= nr) v = 0.0f;  // up to r16: zeros
+            if (GEMM) {
+                __nv_bfloat16 split[3];
+                split_bf16x3(v * scale, split);
+                __nv_bfloat16* dst = a.h_split + (t0 + token) * 2 * a.r16 + r0 + r;
+                dst[0] = split[0];
+                dst[a.r16] = split[1];
+            } else {
+                a.h[(blockIdx.z * a.m + t0 + token) * a.rank + r0 + r] = v;
+            }
+        };
+        // the item's warps add their partial sums, in the order of K
+        cp_async_wait_group<0>();
+        __syncwarp();
+        float* own = reinterpret_cast<float*>(ring_mem);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) red[warp][(h * 4 + n) * 4 + e][lane] = acc[h][n][e];
-        __syncthreads();
-        for (int u = tid; u < 2 * 4 * 4 * 32; u += kThreads) {
-            const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) & 3, h = hne >> 4;
-            const int p = n * 8 + (l & 3) * 2 + (e & 1), r = h * 16 + (e >> 1) * 8 + (l >> 2);
-            if (!(mine >> p & 1u) || (GEMM ? r0 + r >= a.r16 : r >= nr)) continue;
-            float s = 0.0f;
-            if (r < nr) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) s += red[w][hne][l];
-            }
-            if (GEMM) {
-                if (a.scales) s *= a.scales[ad];
-                __nv_bfloat16 part[3];
-                split_bf16x3(s, part);
-                __nv_bfloat16* dst = a.h_split + static_cast<size_t>(t0 + p) * 2 * a.r16 + r0 + r;
-                dst[0] = part[0];
-                dst[a.r16] = part[1];
-            } else {
-                h_out[(t0 + p) * a.rank + r0 + r] = s;
-            }
+                for (int e = 0; e < 4; ++e) own[((h * NT + n) * 4 + e) * 32 + lane] = acc[h][n][e];
+        item_sync(1 + item, ks * 32);
+        const float* parts = reinterpret_cast<const float*>(smem_raw + item * ks * kShrinkStages * kRingBytes);
+        constexpr int kPart = kShrinkStages * kRingBytes / 4;
+        for (int u = part * 32 + lane; u < 2 * NT * 4 * 32; u += ks * 32) {
+            const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) % NT, h = (hne >> 2) / NT;
+            float v = 0.0f;
+            for (int w = 0; w < ks; ++w) v += parts[w * kPart + u];
+            finish(h * 16 + (e >> 1) * 8 + (l >> 2), n * 8 + (l & 3) * 2 + (e & 1), v);
         }
-        __syncthreads();
+        item_sync(1 + item, ks * 32);
     }
 }
 
@@ -212,7 +223,7 @@ struct StreamSmem {
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) lora_stream_kernel(const LoraArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
+    extern __shared__ __align__(128) unsigned char smem_raw[];
     StreamSmem<NT>& sm = *reinterpret_cast<StreamSmem<NT>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c8 = (lane & 3) * 8;
@@ -315,28 +326,40 @@ cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-template <bool GEMM>
+template <bool GEMM, int NT>
 static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
     static PerDeviceOnce once;
-    constexpr int smem = kWarps * 2 * 4 * 4 * 32 * sizeof(float);
+    constexpr int smem = kWarps * kShrinkStages * kRingBytes;
     cudaError_t err = once.run([] {
-        return cudaFuncSetAttribute(lora_shrink_kernel<GEMM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(lora_shrink_kernel<GEMM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err != cudaSuccess) return err;
-    const unsigned groups = static_cast<unsigned>((a.m + kGroup - 1) / kGroup);
-    const unsigned rank_tiles = (a.rank + kRankTile - 1) / kRankTile;
+    const long long groups = (a.m + kGroup - 1) / kGroup;
+    const int rank_tiles = (a.rank + NT * 8 - 1) / (NT * 8);
+    // warps per item: as many (2 to 16) as keep all SMs' warps busy once
+    int ks = 16;
+    while (ks > 2 && groups * rank_tiles * ks > 148 * kWarps) ks /= 2;
+    const unsigned blocks = static_cast<unsigned>((groups * ks + kWarps - 1) / kWarps);
     // a block per adapter for a few tokens, one for all of them when the
     // token groups fill the SMs by themselves
     const unsigned most = static_cast<unsigned>(a.m < kGroup ? a.m : kGroup);
-    unsigned lanes = 296 / (groups * rank_tiles * a.k_splits);
+    unsigned lanes = 148 / (blocks * rank_tiles * a.k_splits);
     lanes = lanes < 1 ? 1 : lanes > most ? most : lanes;
-    lora_shrink_kernel<GEMM><<<dim3(groups, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
-        a, static_cast<int>(rank_tiles));
+    lora_shrink_kernel<GEMM, NT><<<dim3(blocks, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
+        a, rank_tiles, ks);
     return cudaGetLastError();
 }
 
+template <bool GEMM>
+static cudaError_t launch_shrink_rank(const LoraArgs& a, cudaStream_t stream) {
+    if (a.rank <= 8) return launch_shrink<GEMM, 1>(a, stream);
+    if (a.rank <= 16) return launch_shrink<GEMM, 2>(a, stream);
+    if (a.rank <= 32) return launch_shrink<GEMM, 4>(a, stream);
+    return launch_shrink<GEMM, 8>(a, stream);
+}
+
 cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
-    return a.h_split ? launch_shrink<true>(a, stream) : launch_shrink<false>(a, stream);
+    return a.h_split ? launch_shrink_rank<true>(a, stream) : launch_shrink_rank<false>(a, stream);
 }
 
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {

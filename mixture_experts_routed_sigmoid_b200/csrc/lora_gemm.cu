@@ -7,9 +7,9 @@
 // MMAs over both CTAs; each CTA loads its 128 tokens and its half of W's rows,
 // 128 bytes of K per stage).  The adapters enter as more columns of K behind
 // the projection's: for every adapter that occurs among the tile's tokens, its
-// rank columns twice, with A operand rows hi and lo of h, zero for the tokens
-// of other adapters.  So they cost 2 * rank / k of the projection's MMAs per
-// adapter of a tile, and no pass over y.
+// rank columns (rounded up to 16) twice, against the hi and the lo part of h,
+// which are zero for the tokens of other adapters.  So they cost 2 * rank / k of
+// the projection's MMAs per adapter of a tile, and no pass over y.
 //
 // A zero times NaN or infinity is NaN, so a piece of B that is not finite never
 // reaches the tensor core: its writer replaces it by zeros and marks the tile,
@@ -32,17 +32,7 @@ constexpr int kTmemCols = 512;
 constexpr int kFixSlots = 16;
 constexpr int kPitch = 33;            // words of a staged epilogue row
 constexpr int kEpiBytes = 4 * 32 * kPitch * 4;
-constexpr int kSmem = kStages * kStage + kEpiBytes + 512 + 1024;
-
-// Where a tile's adapter columns lie: adapter i's hi columns at i * 2 * r16,
-// its lo columns r16 further (r16: rank rounded up to the MMA's 16 columns).
-struct ExtPiece {
-    int adapter, part, r;  // index in the tile's list, 0 hi / 1 lo, first rank column
-};
-__device__ __forceinline__ ExtPiece ext_piece(int col, int r16) {
-    const int adapter = col / (2 * r16), rem = col - adapter * 2 * r16;
-    return ExtPiece{adapter, rem >= r16, rem >= r16 ? rem - r16 : rem};
-}
+constexpr int kSmem = kStages * kStage + kEpiBytes + 512 + kLoraTileRows * 4 + 1024;
 
 __device__ __forceinline__ bool not_finite_bf16x8(const uint4& v) {
     bool bad = false;
@@ -57,6 +47,7 @@ __device__ __forceinline__ bool not_finite_bf16x8(const uint4& v) {
 // they go on or stop together.
 __device__ __forceinline__ bool all_of_four_warps(bool v) {
     int r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
@@ -102,13 +93,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // tile's place in this pair's sequence modulo kFixSlots.  The writers are
     // at most kStages stages and two accumulators ahead of the epilogue.
     volatile int* fix = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    int* list = const_cast<int*>(fix) + kFixSlots;  // [kLoraTileRows] the tile's adapters
     float* epi = reinterpret_cast<float*>(smem + kStages * kStage);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 2);   // one arrival from each CTA
+            mbar_init(&full[s], 2);   // both by the leader's copies, or one by each CTA's adapter writers
             mbar_init(&empty[s], 1);
             mbar_init(&grant[s], 1);
         }
@@ -156,7 +148,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
                     const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
                     uint8_t* sa = smem + stage * kStage;
-                    mbar_arrive_expect_tx_cluster(bar, kHalf + half * 128);
+                    if (rank == 0) {  // for both CTAs' copies; the stage's second arrival too
+                        mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
+                        mbar_arrive(&full[stage]);
+                    }
                     tma_load_2d_pair(sa, &map_x, bar, kb * 64, mt * 256 + static_cast<int>(rank) * 128);
                     tma_load_2d_pair(sa + kHalf, &map_w, bar, kb * 64, nt * bn + static_cast<int>(rank) * half);
                     advance(stage, phase, 1);
@@ -216,64 +211,96 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     } else if (warp >= 8) {
         // ------------------------------------------------------ adapters' stages
         wait_for_previous_kernel();
+        // Two stages of copies are in flight before the first is handed on, so a
+        // tile with many adapters does not wait for each copy's latency.
         const int row = tid - 256;  // 0..127: this CTA's token row and its W row of the tile
+        const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row * 128);
+        const auto piece_at = [&](int p) { return static_cast<uint32_t>((p ^ (row & 7)) << 4); };
         int stage = 0, seq = 0;
         uint32_t granted = 0;  // bit s: parity of grant[s]'s next phase
         bool good = true;
         for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
             const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
             stage = (stage + nk) % kStages;
+            const int count = a.tile_count[mt];
+            all_of_four_warps(true);  // the last tile's list is read
+            for (int i = row; i < count; i += 128)
+                list[i] = a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + i];
+            all_of_four_warps(true);
             const long long t = static_cast<long long>(mt) * 256 + rank * 128 + row;
             const int id = t < a.m ? a.adapter_ids[t] : -1;
             const int col = nt * bn + static_cast<int>(rank) * half + row;
             const bool col_in = row < half && col < a.n;
-            const int* list = a.tile_list + static_cast<size_t>(mt) * kLoraTileRows;
-            const int cols = ext_steps(mt) * 16;
-            for (int c0 = 0; c0 < cols; c0 += 64) {
-                uint4 va[8], vb[8];
+            const __nv_bfloat16* h_row = a.h_split + (t < a.m ? t : 0) * 2 * a.r16;
+            const __nv_bfloat16* b_row = a.B + static_cast<size_t>(col_in ? col : 0) * a.rank;
+            const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
+            const int cols = count * 2 * a.r16;
+
+            // Hands stage `st` on: its copies have landed; pieces of B that are
+            // not finite become zeros (the epilogue adds their products).
+            const auto hand_on = [&](int st) {
                 bool bad = false;
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    va[p] = vb[p] = make_uint4(0u, 0u, 0u, 0u);
-                    if (c0 + p * 8 >= cols) continue;
-                    const ExtPiece e = ext_piece(c0 + p * 8, a.r16);
-                    const int ad = list[e.adapter];
-                    if (ad == id)
-                        va[p] = *reinterpret_cast<const uint4*>(
-                            a.h_split + (static_cast<size_t>(t) * 2 + e.part) * a.r16 + e.r);
-                    if (col_in && e.r < a.rank)
-                        vb[p] = *reinterpret_cast<const uint4*>(
-                            a.B + (static_cast<size_t>(ad) * a.n + col) * a.rank + e.r);
-                }
-#pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    if (not_finite_bf16x8(vb[p])) {
-                        vb[p] = make_uint4(0u, 0u, 0u, 0u);
-                        bad = true;
-                    }
-                good = __all_sync(0xffffffffu, mbar_wait(&grant[stage], granted >> stage & 1u, ctl));
-                granted ^= 1u << stage;
-                if (good) {
-                    uint8_t* sa = smem + stage * kStage;
+                if (row < half) {
 #pragma unroll
                     for (int p = 0; p < 8; ++p) {
-                        const int off = row * 128 + ((p ^ (row & 7)) << 4);
-                        *reinterpret_cast<uint4*>(sa + off) = va[p];
-                        if (row < half) *reinterpret_cast<uint4*>(sa + kHalf + off) = vb[p];
+                        uint4* at = reinterpret_cast<uint4*>(smem + st * kStage + kHalf + row * 128 + piece_at(p));
+                        if (not_finite_bf16x8(*at)) {
+                            *at = make_uint4(0u, 0u, 0u, 0u);
+                            bad = true;
+                        }
                     }
-                    if (bad) {
-                        const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
-                        st_shared_cluster(cluster_addr(at, 0), tile + 1);
-                        st_shared_cluster(cluster_addr(at, 1), tile + 1);
-                    }
-                    fence_proxy_async_smem();
                 }
-                good = all_of_four_warps(good);
+                if (bad) {
+                    const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
+                    st_shared_cluster(cluster_addr(at, 0), tile + 1);
+                    st_shared_cluster(cluster_addr(at, 1), tile + 1);
+                }
+                fence_proxy_async_smem();
+                all_of_four_warps(true);
+                if (row == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st]), 0));
+            };
+            int ad = 0, rem = 0;       // adapter of the list and column within its 2 * r16
+            int older = -1, newer = -1;  // stages whose copies are in flight
+            for (int c0 = 0; c0 < cols; c0 += 64) {
+                good = all_of_four_warps(mbar_wait(&grant[stage], granted >> stage & 1u, ctl));
                 if (!good) break;
-                if (row == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full[stage]), 0));
+                granted ^= 1u << stage;
+                const uint32_t sa = ext + static_cast<uint32_t>(stage * kStage);
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const bool in = ad < count;
+                    const int adapter = in ? list[ad] : 0;
+                    const int r = rem < a.r16 ? rem : rem - a.r16;
+                    const bool use_a = in && adapter == id, use_b = in && col_in && r < a.rank;
+                    cp_async_16(sa + piece_at(p), use_a ? h_row + rem : a.h_split, use_a ? 16u : 0u);
+                    if (row < half)
+                        cp_async_16(sa + kHalf + piece_at(p), use_b ? b_row + adapter * b_adapter + r : a.B,
+                                    use_b ? 16u : 0u);
+                    rem += 8;
+                    if (rem == 2 * a.r16) {
+                        rem = 0;
+                        ++ad;
+                    }
+                }
+                cp_async_commit();
+                if (older >= 0) {
+                    cp_async_wait_group<2>();
+                    hand_on(older);
+                }
+                older = newer;
+                newer = stage;
                 stage = (stage + 1) % kStages;
             }
+            if (good && older >= 0) {
+                cp_async_wait_group<1>();
+                hand_on(older);
+            }
+            if (good && newer >= 0) {
+                cp_async_wait_group<0>();
+                hand_on(newer);
+            }
         }
+        cp_async_wait_all();
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue
         wait_for_previous_kernel();

@@ -68,13 +68,6 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Copies one step into the ring slot at `slot`: columns [k0, k0 + 64 or 128)
 // of the tile's rows.  row(r) gives the global address of ring row r, or null
 // for a row that the tile does not have (its slot keeps what it held: rows
