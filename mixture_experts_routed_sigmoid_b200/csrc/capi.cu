@@ -1049,15 +1049,20 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.r16 = L.r16;
     a.wait_limit_ns = moe::kDefaultWaitLimitNs;
     const int bn = stream_w ? 0 : lora_tile_columns(m, n);
-    CUtensorMap map_x, map_w;
-    if (!stream_w) {
+    cudaError_t err;
+    if (stream_w) {
+        err = moe::launch_lora_shrink(a, s);
+        if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
+        err = moe::launch_lora_stream(a, num_sms(), s);
+    } else {
+        CUtensorMap map_x, map_w, map_a;
         MOE_TRY(make_map(&map_x, x, k, m, 128, "x"));
         MOE_TRY(make_map(&map_w, W, k, n, bn / 2, "W"));
+        MOE_TRY(make_map(&map_a, A, k, static_cast<unsigned long long>(n_adapters) * rank, rank, "A"));
+        err = moe::launch_lora_shrink_gemm(a, map_x, map_a, s);
+        if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
+        err = moe::launch_lora_gemm(a, map_x, map_w, bn, num_sms(), s);
     }
-    cudaError_t err = moe::launch_lora_shrink(a, s);
-    if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
-    err = stream_w ? moe::launch_lora_stream(a, num_sms(), s)
-                   : moe::launch_lora_gemm(a, map_x, map_w, bn, num_sms(), s);
     if (err != cudaSuccess) return cuda_fail(err, "projection launch");
     return ok();
 }

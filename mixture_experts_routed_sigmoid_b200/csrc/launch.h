@@ -221,6 +221,9 @@ struct LoraArgs {
 };
 cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream);
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream);
+// map_x: boxes of 128 rows; map_a: of `rank` rows of [n_adapters * rank, k].
+cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_a,
+                                    cudaStream_t stream);
 // map_x: boxes of 128 rows, map_w: boxes of bn / 2 rows (64 columns each).
 cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
                              int num_sms, cudaStream_t stream);

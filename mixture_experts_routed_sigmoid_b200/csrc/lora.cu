@@ -3,16 +3,15 @@
 //   y[t] = W x[t] + scales[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
 // (a = -1: the projection alone).
 //
-// Kernel 1 (shrink): h[t] = A[a] x[t].  An item is 32 consecutive tokens and
+// Kernel 1 (shrink), m <= 64: h[t] = A[a] x[t].  An item is 32 consecutive tokens and
 //   one of the adapters that occur among them; only those tokens' rows of x
 //   are read.  The tokens are the rows of the MMA (stream_mma.cuh, with x in
 //   the place of the weights), the adapter's rank its columns; rows of other
 //   tokens are dropped by selection, never by a multiplication with zero, so
 //   an adapter that holds NaN or infinities reaches its own requests only.
-//   It reads x once from HBM, where the projection then finds it in the L2.
 // Kernel 2, m <= 64: streams W once through mma.sync (stream_mma.cuh) and
 //   adds scales[a] * B[a] h in its epilogue.
-// Kernel 2, larger m: the tcgen05 GEMM of lora_gemm.cu.
+// Larger m: the two tcgen05 kernels of lora_gemm.cu.
 #include "launch.h"
 #include "stream_mma.cuh"
 
@@ -29,21 +28,18 @@ constexpr int kTileN = 32;    // output columns of a streaming tile
 // grid: (token groups / groups per block, rank tiles x adapter lanes, K
 // ranges).  `ks` warps split the K of an item; a block holds 16 / ks token
 // groups.  Adapter lane j of L takes every L-th adapter of its tokens.  The
-// streaming kernel gets the f32 sums, K range z at h + z * m * rank (it adds
-// the ranges in order); the GEMM gets them scaled and split into two bf16
-// parts, with the list of the adapters that occur in each of its row tiles.
+// f32 sums of K range z go to h + z * m * rank; the reader adds the ranges in
+// order.
 constexpr int kShrinkStages = 3;
 
 __device__ __forceinline__ void item_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-template <bool GEMM, int NT>  // NT: groups of 8 rank rows per item
+template <int NT>  // NT: groups of 8 rank rows per item
 __global__ void __launch_bounds__(kThreads, 1)
     lora_shrink_kernel(const LoraArgs a, int rank_tiles, int ks) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    __shared__ __align__(16) int s_tile[kLoraTileRows];
-    __shared__ int s_count[kLoraTileRows / 32];
     __shared__ int s_bad;
     allow_next_kernel();  // it waits for this one's writes before it reads them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -62,44 +58,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
     }
-    const int block_tokens = kWarps / ks * kGroup;  // 32 to 256
-    const long long first = static_cast<long long>(blockIdx.x) * block_tokens;
-    if (GEMM && blockIdx.y == 0 && first % kLoraTileRows == 0) {
-        // the adapters of the row tile that begins here, in order of their first token
-        int id = -1;
-        if (tid < kLoraTileRows) {
-            if (first + tid < a.m) id = a.adapter_ids[first + tid];
-            if (id >= a.n_adapters) id = -1;
-            s_tile[tid] = id;
-        }
-        __syncthreads();
-        bool opens = false;
-        unsigned ballot = 0;
-        if (tid < kLoraTileRows) {
-            const unsigned twins = __match_any_sync(0xffffffffu, id);  // every lane takes part
-            opens = id >= 0 && __ffs(twins) - 1 == lane;
-            for (int j = 0; j < warp * 8; ++j) {
-                const int4 v = reinterpret_cast<const int4*>(s_tile)[j];
-                opens = opens && v.x != id && v.y != id && v.z != id && v.w != id;
-            }
-            ballot = __ballot_sync(0xffffffffu, opens);
-            if (lane == 0) s_count[warp] = __popc(ballot);
-        }
-        __syncthreads();
-        const int mt = static_cast<int>(first / kLoraTileRows);
-        if (tid < kLoraTileRows) {
-            int before = 0, total = 0;
-            for (int w = 0; w < kLoraTileRows / 32; ++w) {
-                if (w < warp) before += s_count[w];
-                total += s_count[w];
-            }
-            if (opens)
-                a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + before + __popc(ballot & lanemask_lt())] = id;
-            if (tid == 0) a.tile_count[mt] = total;
-        }
-    }
     const int item = warp / ks, part = warp % ks;  // this warp's tokens and its share of K
-    const long long t0 = first + item * kGroup;
+    const long long t0 = static_cast<long long>(blockIdx.x) * (kWarps / ks * kGroup) + item * kGroup;
     int my_id = t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
     if (my_id >= a.n_adapters) my_id = -1;  // reported above; no adapter is read for it
     // lanes that open an adapter: the first token of each distinct id
@@ -120,7 +80,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j % adapter_lanes != my_lane) continue;
         const int ad = __shfl_sync(0xffffffffu, my_id, lead);
         const unsigned mine = __ballot_sync(0xffffffffu, my_id == ad);  // tokens of this adapter
-        const float scale = GEMM && a.scales ? a.scales[ad] : 1.0f;
         const __nv_bfloat16* A = a.A + (static_cast<size_t>(ad) * a.rank + r0) * a.k;
         const __nv_bfloat16* tok[NT];
 #pragma unroll
@@ -152,21 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
             use_slot = use_slot + 1 == kShrinkStages ? 0 : use_slot + 1;
         }
-        // element (h, n, e): token h * 16 + (e / 2) * 8 + g, rank row n * 8 + 2 c + e % 2
-        const auto finish = [&](int token, int r, float v) {
-            if (!(mine >> token & 1u) || (GEMM ? r0 + r >= a.r16 : r >= nr)) return;
-            if (r >= nr) v = 0.0f;  // up to r16: zeros
-            if (GEMM) {
-                __nv_bfloat16 split[3];
-                split_bf16x3(v * scale, split);
-                __nv_bfloat16* dst = a.h_split + (t0 + token) * 2 * a.r16 + r0 + r;
-                dst[0] = split[0];
-                dst[a.r16] = split[1];
-            } else {
-                a.h[(blockIdx.z * a.m + t0 + token) * a.rank + r0 + r] = v;
-            }
-        };
-        // the item's warps add their partial sums, in the order of K
+        // the item's warps add their partial sums, in the order of K; element
+        // (h, n, e): token h * 16 + (e / 2) * 8 + g, rank row n * 8 + 2 c + e % 2
         cp_async_wait_group<0>();
         __syncwarp();
         float* own = reinterpret_cast<float*>(ring_mem);
@@ -183,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) % NT, h = (hne >> 2) / NT;
             float v = 0.0f;
             for (int w = 0; w < ks; ++w) v += parts[w * kPart + u];
-            finish(h * 16 + (e >> 1) * 8 + (l >> 2), n * 8 + (l & 3) * 2 + (e & 1), v);
+            const int token = h * 16 + (e >> 1) * 8 + (l >> 2), r = n * 8 + (l & 3) * 2 + (e & 1);
+            if ((mine >> token & 1u) && r < nr) a.h[(blockIdx.z * a.m + t0 + token) * a.rank + r0 + r] = v;
         }
         item_sync(1 + item, ks * 32);
     }
@@ -326,12 +273,12 @@ cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-template <bool GEMM, int NT>
+template <int NT>
 static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
     static PerDeviceOnce once;
     constexpr int smem = kWarps * kShrinkStages * kRingBytes;
     cudaError_t err = once.run([] {
-        return cudaFuncSetAttribute(lora_shrink_kernel<GEMM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(lora_shrink_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err != cudaSuccess) return err;
     const long long groups = (a.m + kGroup - 1) / kGroup;
@@ -345,21 +292,16 @@ static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
     const unsigned most = static_cast<unsigned>(a.m < kGroup ? a.m : kGroup);
     unsigned lanes = 148 / (blocks * rank_tiles * a.k_splits);
     lanes = lanes < 1 ? 1 : lanes > most ? most : lanes;
-    lora_shrink_kernel<GEMM, NT><<<dim3(blocks, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
+    lora_shrink_kernel<NT><<<dim3(blocks, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
         a, rank_tiles, ks);
     return cudaGetLastError();
 }
 
-template <bool GEMM>
-static cudaError_t launch_shrink_rank(const LoraArgs& a, cudaStream_t stream) {
-    if (a.rank <= 8) return launch_shrink<GEMM, 1>(a, stream);
-    if (a.rank <= 16) return launch_shrink<GEMM, 2>(a, stream);
-    if (a.rank <= 32) return launch_shrink<GEMM, 4>(a, stream);
-    return launch_shrink<GEMM, 8>(a, stream);
-}
-
 cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
-    return a.h_split ? launch_shrink_rank<true>(a, stream) : launch_shrink_rank<false>(a, stream);
+    if (a.rank <= 8) return launch_shrink<1>(a, stream);
+    if (a.rank <= 16) return launch_shrink<2>(a, stream);
+    if (a.rank <= 32) return launch_shrink<4>(a, stream);
+    return launch_shrink<8>(a, stream);
 }
 
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {

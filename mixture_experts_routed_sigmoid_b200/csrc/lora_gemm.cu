@@ -16,8 +16,9 @@
 // and the epilogue adds the piece's products for the tokens that do use it.
 //
 // Warps per CTA: 0 copies the tiles (TMA), 1 issues the MMAs (leader CTA only),
-// 4-7 epilogue, 8-11 write the adapters' stages.  Two accumulators let the
-// epilogue of a tile overlap the next tile's MMAs.  Every wait is bounded.
+// 2 and 3 announce the adapters' stages to the leader, 4-7 epilogue, 8-11 write
+// the adapters' stages.  Two accumulators let the epilogue of a tile overlap
+// the next tile's MMAs.  Every wait is bounded.
 #include "launch.h"
 #include "pair_mma.cuh"
 
@@ -87,7 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint64_t* acc_full = empty + kStages;   // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2], leader's are used
     uint64_t* grant = acc_empty + 2;        // [kStages] an empty stage handed to the adapters' writers
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(grant + kStages);
+    uint64_t* written = grant + kStages;    // [2][kStages] a stage that the adapters' writers have filled
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(written + 2 * kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // Tiles (1 + index) that hold a piece of B which is not finite, at the
     // tile's place in this pair's sequence modulo kFixSlots.  The writers are
@@ -103,6 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&full[s], 2);   // both by the leader's copies, or one by each CTA's adapter writers
             mbar_init(&empty[s], 1);
             mbar_init(&grant[s], 1);
+            mbar_init(&written[s], 128);
+            mbar_init(&written[kStages + s], 128);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -130,10 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int half = bn / 2;
     // stages of the adapters' columns of row tile mt (the shrink kernel has run)
     const auto ext_steps = [&](int mt) { return a.tile_count[mt] * 2 * (a.r16 / 16); };  // MMA steps of 16
-    const auto advance = [](int& stage, uint32_t& phase, int by) {
-        stage += by;
-        phase ^= static_cast<uint32_t>(stage / kStages) & 1u;
-        stage %= kStages;
+    const auto advance = [](int& stage, uint32_t& phase) {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
     };
 
     if (warp == 0) {
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     tma_load_2d_pair(sa, &map_x, bar, kb * 64, mt * 256 + static_cast<int>(rank) * 128);
                     tma_load_2d_pair(sa + kHalf, &map_w, bar, kb * 64, nt * bn + static_cast<int>(rank) * half);
-                    advance(stage, phase, 1);
+                    advance(stage, phase);
                 }
                 if (!good) break;
                 // This thread alone follows every phase of `empty` (a parity
@@ -164,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int e = (ext_steps(mt) + 3) / 4; e > 0; --e) {
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
                     mbar_arrive(&grant[stage]);
-                    advance(stage, phase, 1);
+                    advance(stage, phase);
                 }
             }
         }
@@ -177,34 +182,65 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // instruction descriptor: M = 256, N = bn
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                    (static_cast<uint32_t>(bn >> 3) << 17) | ((256u >> 4) << 24);
+            // the start address is the descriptor's low 14 bits (in 16 bytes); all
+            // of the ring lies below 2^18, so additions never carry out of it
+            const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
             bool good = true;
             for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
                 if (!(good = mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl))) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-                int steps = nk * 4, ext = -1;
-                for (int done = 0; done < steps || ext < 0;) {
-                    if (done == steps) {  // the projection is issued; now the adapters
-                        wait_for_previous_kernel();
-                        ext = ext_steps(tile / n_col_tiles);
-                        steps += ext;
-                        continue;
-                    }
+                // The issue loop has to keep ahead of MMAs of 128 cycles: whole
+                // stages are unrolled, descriptors differ by an addition.
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!(good = mbar_wait(&full[stage], phase, ctl))) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4)
+                        umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
+                    umma_commit_pair(&empty[stage]);
+                    advance(stage, phase);
+                }
+                if (!good) break;
+                wait_for_previous_kernel();
+                for (int left = ext_steps(tile / n_col_tiles); left > 0; left -= 4) {
                     if (!(good = mbar_wait_cluster(&full[stage], phase, ctl))) break;
                     tc_fence_after_sync();
-                    const uint32_t sa = smem_u32(smem + stage * kStage);
-                    const int here = min(4, steps - done);
-                    for (int k4 = 0; k4 < here; ++k4)
-                        umma_bf16_pair(d, sw128_kmajor_desc(sa + k4 * 32),
-                                       sw128_kmajor_desc(sa + kHalf + k4 * 32), idesc, (done + k4) != 0);
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+                    for (int k4 = 0; k4 < min(4, left); ++k4)
+                        umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
                     umma_commit_pair(&empty[stage]);
-                    done += here;
-                    advance(stage, phase, 1);
+                    advance(stage, phase);
                 }
                 if (!good) break;
                 umma_commit_pair(&acc_full[acc]);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------------ announcing them
+        // A release at cluster scope waits for its thread's copies in flight, so
+        // threads without any make it, for every other stage each (with barriers
+        // of their own: each sees every phase that it has to count).
+        if (lane == 0) {
+            wait_for_previous_kernel();
+            int stage = 0, n = 0;
+            uint32_t seen = 0;  // bit s: parity of this thread's next phase of stage s
+            uint64_t* mine = written + (warp - 2) * kStages;
+            bool good = true;
+            for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
+                stage = (stage + nk) % kStages;
+                for (int e = (ext_steps(tile / n_col_tiles) + 3) / 4; e > 0; --e, ++n) {
+                    if ((n & 1) == warp - 2) {
+                        if (!(good = mbar_wait(&mine[stage], seen >> stage & 1u, ctl))) break;
+                        seen ^= 1u << stage;
+                        mbar_arrive_cluster(cluster_addr(smem_u32(&full[stage]), 0));
+                    }
+                    stage = stage + 1 == kStages ? 0 : stage + 1;
+                }
             }
         }
         __syncwarp();
@@ -216,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int row = tid - 256;  // 0..127: this CTA's token row and its W row of the tile
         const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row * 128);
         const auto piece_at = [&](int p) { return static_cast<uint32_t>((p ^ (row & 7)) << 4); };
-        int stage = 0, seq = 0;
+        int stage = 0, seq = 0, handed = 0;
         uint32_t granted = 0;  // bit s: parity of grant[s]'s next phase
         bool good = true;
         for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
@@ -256,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     st_shared_cluster(cluster_addr(at, 1), tile + 1);
                 }
                 fence_proxy_async_smem();
-                all_of_four_warps(true);
-                if (row == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st]), 0));
+                mbar_arrive(&written[(handed++ & 1) * kStages + st]);
             };
             int ad = 0, rem = 0;       // adapter of the list and column within its 2 * r16
             int older = -1, newer = -1;  // stages whose copies are in flight
@@ -397,7 +432,253 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
 }
 
+// ------------------------------------------------------------------ shrink
+// h[t] = scales[a] * (A[a] x[t]) for 128 tokens and one adapter at a time:
+// M = 128 tokens, N = the rank rounded up to 16, one tcgen05 accumulator.  Rows
+// of tokens with another adapter are computed along and dropped.  grid: (token
+// tiles x cluster, adapter lanes): lane j of L takes every L-th adapter of its
+// tokens, the CTAs of a cluster split K and add their sums in rank order over
+// distributed shared memory.  Reads x once from HBM (16384 tokens of 2048: 11
+// us), where the projection then finds it in the L2.  Also writes the call's
+// status word and the adapters of every 256-token row tile.
+constexpr int kShrinkStages = 4;
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkPitch = MOE_MAX_LORA_RANK + 1;
+constexpr int kShrinkSmem = kShrinkStages * kStage + 128 * kShrinkPitch * 4 + 256 + 1024;
+
+// Distinct ids >= 0 of the first n threads' `id` (n a multiple of 32), in the
+// order of their first thread, into list; returns their number in every thread.
+// The block's threads all call it; ids: scratch of n ints, counts: of n / 32.
+__device__ __forceinline__ int distinct_ids(int id, int n, int* ids, int* counts, int* list) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < n) ids[tid] = id;
+    __syncthreads();
+    const unsigned twins = __match_any_sync(0xffffffffu, id);  // every lane takes part
+    bool opens = tid < n && id >= 0 && __ffs(twins) - 1 == lane;
+    if (tid < n)
+#pragma unroll 8
+        for (int j = 0; j < warp * 8; ++j) {
+            const int4 v = reinterpret_cast<const int4*>(ids)[j];
+            opens = opens && v.x != id && v.y != id && v.z != id && v.w != id;
+        }
+    const unsigned ballot = __ballot_sync(0xffffffffu, opens);
+    if (tid < n && lane == 0) counts[warp] = __popc(ballot);
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < n / 32; ++w) {
+        if (w < warp) before += counts[w];
+        total += counts[w];
+    }
+    if (opens) list[before + __popc(ballot & lanemask_lt())] = id;
+    __syncthreads();
+    return total;
+}
+
+__global__ void __launch_bounds__(kShrinkThreads, 1)
+    lora_shrink_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
+                            const __grid_constant__ CUtensorMap map_a, const LoraArgs a, int split) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    float* sums = reinterpret_cast<float*>(smem + kShrinkStages * kStage);  // [128][kShrinkPitch]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sums + 128 * kShrinkPitch);
+    uint64_t* empty = full + kShrinkStages;
+    uint64_t* acc_full = empty + kShrinkStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    __shared__ __align__(16) int s_id[kLoraTileRows];
+    __shared__ int s_list[kLoraTileRows], s_count[kLoraTileRows / 32], s_bad;
+
+    allow_next_kernel();  // it waits for this one's writes before it reads them
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(blockIdx.x) % split, mt = static_cast<int>(blockIdx.x) / split;
+    const long long t0 = static_cast<long long>(mt) * 128;
+    if (tid == 0) {
+        for (int s = 0; s < kShrinkStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        s_bad = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&map_x);
+        prefetch_tensormap(&map_a);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, MOE_MAX_LORA_RANK);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, nullptr, a.wait_limit_ns};
+
+    const auto id_of = [&](long long t) {
+        const int id = t < a.m ? a.adapter_ids[t] : -1;
+        return id < a.n_adapters ? id : -1;  // out of range: reported below, no adapter is read for it
+    };
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        bool bad = false;
+        const auto check = [&](int id) { bad |= id < -1 || id >= a.n_adapters; };
+        const int* ids = a.adapter_ids;
+        const long long vec = reinterpret_cast<uintptr_t>(ids) % 16 ? 0 : a.m / 4;
+#pragma unroll 8
+        for (long long i = tid; i < vec; i += kShrinkThreads) {
+            const int4 v = reinterpret_cast<const int4*>(ids)[i];
+            check(v.x);
+            check(v.y);
+            check(v.z);
+            check(v.w);
+        }
+        for (long long t = vec * 4 + tid; t < a.m; t += kShrinkThreads) check(ids[t]);
+        if (bad) s_bad = 1;
+        __syncthreads();
+        if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
+    }
+    if (blockIdx.y == 0 && rank == 0 && mt % 2 == 0) {
+        const int n = distinct_ids(id_of(t0 + tid), kLoraTileRows, s_id, s_count,
+                                   a.tile_list + static_cast<size_t>(mt / 2) * kLoraTileRows);
+        if (tid == 0) a.tile_count[mt / 2] = n;
+    }
+    const int my_id = tid < 128 ? id_of(t0 + tid) : -1;
+    const int n_list = distinct_ids(my_id, 128, s_id, s_count, s_list);  // s_id: the tile's ids
+
+    const int nkb = (a.k + 63) / 64;
+    const int kb_lo = nkb * rank / split, kb_hi = nkb * (rank + 1) / split;
+    const uint32_t bytes = kHalf + static_cast<uint32_t>(a.rank) * 128;
+    const uint32_t idesc = umma_idesc_bf16_f32(128, a.r16);
+    const int chunks = (a.r16 + 31) / 32;
+    int stage = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    const auto advance = [&] {
+        if (++stage == kShrinkStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    // A CTA that gave up goes through the same cluster barriers as the others.
+    for (int j = blockIdx.y; j < n_list; j += gridDim.y) {
+        const int ad = s_list[j];
+        if (warp == 0) {
+            if (lane == 0)
+                for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1, ctl)) break;
+                    uint8_t* sa = smem + stage * kStage;
+                    mbar_arrive_expect_tx(&full[stage], bytes);
+                    tma_load_2d(sa, &map_x, &full[stage], kb * 64, static_cast<int>(t0));
+                    tma_load_2d(sa + kHalf, &map_a, &full[stage], kb * 64, ad * a.rank);
+                    advance();
+                }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+                bool good = true;
+                for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                    if (!(good = mbar_wait(&full[stage], phase, ctl))) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4)
+                        umma_bf16(tmem, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, kb > kb_lo || k4 > 0);
+                    umma_commit(&empty[stage]);
+                    advance();
+                }
+                if (good) umma_commit(acc_full);
+            }
+        } else if (warp >= 4) {
+            const bool good = __all_sync(0xffffffffu, mbar_wait(acc_full, acc_phase, ctl));
+            tc_fence_after_sync();
+            if (good)
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t v[32];
+                    tmem_load_32cols(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c * 32, v);
+                    tmem_load_wait();
+                    float* row = sums + ((warp & 3) * 32 + lane) * kShrinkPitch + c * 32;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) row[i] = __uint_as_float(v[i]);
+                }
+            tc_fence_before_sync();
+            acc_phase ^= 1;
+        }
+        __syncwarp();
+        if (split > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        // this CTA's rows of the tile: the partial sums of all CTAs, in rank order
+        const float scale = a.scales ? a.scales[ad] : 1.0f;
+        const int r_lo = 128 * rank / split, r_hi = 128 * (rank + 1) / split;
+        for (int u = tid; u < (r_hi - r_lo) * a.r16; u += kShrinkThreads) {
+            const int row = r_lo + u / a.r16, r = u % a.r16;
+            if (s_id[row] != ad) continue;
+            float v = 0.0f;
+            if (r < a.rank) {
+                const uint32_t at = smem_u32(sums + row * kShrinkPitch + r);
+                for (int q = 0; q < split; ++q) v += split > 1 ? ld_shared_cluster(cluster_addr(at, q)) : sums[row * kShrinkPitch + r];
+            }
+            v *= scale;
+            // hi + lo: 16 significant bits; a value that is not finite is its own hi part
+            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+            const float hf = __bfloat162float(hi);
+            __nv_bfloat16* dst = a.h_split + (t0 + row) * 2 * a.r16 + r;
+            dst[0] = hi;
+            dst[a.r16] = __float2bfloat16_rn(fabsf(hf) <= 3.4e38f ? v - hf : 0.0f);
+        }
+        // the sums are read; the accumulator is free
+        if (split > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+        tc_fence_after_sync();
+    }
+    if (*abort_flag && tid == 0) {
+        set_status(a.status, kDevTimeout);
+        const uint64_t start = global_timer_ns();  // copies in flight land
+        while (global_timer_ns() - start < 1000000ull) {
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, MOE_MAX_LORA_RANK);
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_a,
+                                    cudaStream_t stream) {
+    static PerDeviceOnce once;
+    cudaError_t err = once.run([] {
+        return cudaFuncSetAttribute(lora_shrink_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kShrinkSmem);
+    });
+    if (err != cudaSuccess) return err;
+    // K split over as many CTAs (1 to 8, at least four stages each) as 148 SMs
+    // hold once, then adapter lanes for what is left of them
+    const long long tiles = (a.m + 127) / 128;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 148 && (a.k + 63) / 64 >= split * 8) split *= 2;
+    const long long rest = 148 / (tiles * split);
+    const unsigned lanes = static_cast<unsigned>(rest < 1 ? 1 : rest > 128 ? 128 : rest);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), lanes);
+    cfg.blockDim = dim3(kShrinkThreads);
+    cfg.dynamicSmemBytes = kShrinkSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_shrink_gemm_kernel, map_x, map_a, a, split);
+}
 
 cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
                              int num_sms, cudaStream_t stream) {

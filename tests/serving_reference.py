@@ -89,7 +89,7 @@ def lora(x, W, ids, A, B, scales, bf16_out):
         Ad, Bd = A[a].double(), B[a].double()
         s = scales[a].double() if scales is not None else torch.tensor(1.0, dtype=torch.float64)
         h = xd[t] @ Ad.T
-        dh = (dot_gamma(k) + 8 * U) * (xd[t].abs() @ Ad.abs().T)
+        dh = (4 * -(-k // 16) + 24) * U * (xd[t].abs() @ Ad.abs().T)  # one chain, as the projection
         y[t] += s * (h @ Bd.T)
         # h enters its product with 16 significant bits or more; rank sequential additions
         dy[t] += s.abs() * (dh @ Bd.abs().T + (2.0 ** -17 + (rank + 8) * U) * (h.abs() @ Bd.abs().T))
