@@ -16,8 +16,11 @@
 // and the epilogue adds the piece's products for the tokens that do use it.
 //
 // Warps per CTA: 0 copies the tiles (TMA), 1 issues the MMAs (leader CTA only),
-// 2 and 3 announce the adapters' stages to the leader, 4-7 epilogue, 8-11 write
-// the adapters' stages.  Two accumulators let the epilogue of a tile overlap
+// 2 and 3 check the adapters' stages and announce them to the leader, 4-7
+// epilogue, 8-11 copy the adapters' stages (cp.async: 16-byte pieces of h and B
+// picked by adapter).  A fence or a release waits for its thread's copies in
+// flight, so the threads that copy never fence: that alone took a stage from
+// 3100 cycles to its MMAs' time.  Two accumulators let the epilogue of a tile overlap
 // the next tile's MMAs.  Every wait is bounded.
 #include "launch.h"
 #include "pair_mma.cuh"
@@ -88,8 +91,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint64_t* acc_full = empty + kStages;   // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2], leader's are used
     uint64_t* grant = acc_empty + 2;        // [kStages] an empty stage handed to the adapters' writers
-    uint64_t* written = grant + kStages;    // [2][kStages] a stage that the adapters' writers have filled
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(written + 2 * kStages);
+    uint64_t* landed = grant + kStages;    // [2][kStages] an adapters' stage whose copies have landed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 2 * kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // Tiles (1 + index) that hold a piece of B which is not finite, at the
     // tile's place in this pair's sequence modulo kFixSlots.  The writers are
@@ -105,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&full[s], 2);   // both by the leader's copies, or one by each CTA's adapter writers
             mbar_init(&empty[s], 1);
             mbar_init(&grant[s], 1);
-            mbar_init(&written[s], 128);
-            mbar_init(&written[kStages + s], 128);
+            mbar_init(&landed[s], 128);  // the copying threads
+            mbar_init(&landed[kStages + s], 128);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -132,8 +135,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const int cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
     const int nk = (a.k + 63) / 64;
     const int half = bn / 2;
-    // stages of the adapters' columns of row tile mt (the shrink kernel has run)
-    const auto ext_steps = [&](int mt) { return a.tile_count[mt] * 2 * (a.r16 / 16); };  // MMA steps of 16
+    // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
+    // must have finished: waited for behind the first tile's projection, and
+    // from the second tile on the count is loaded ahead of the tile.
+    const auto ext_steps = [&](int tile) { return a.tile_count[tile / n_col_tiles] * 2 * (a.r16 / 16); };
     const auto advance = [](int& stage, uint32_t& phase) {
         if (++stage == kStages) {
             stage = 0;
@@ -149,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool good = true;
             for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
                 const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
+                int steps = tile == cluster ? 0 : ext_steps(tile);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
                     const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
@@ -165,8 +171,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 // This thread alone follows every phase of `empty` (a parity
                 // names a phase only to a waiter that is at most one behind);
                 // it hands the adapters' stages to their writers.
-                wait_for_previous_kernel();
-                for (int e = (ext_steps(mt) + 3) / 4; e > 0; --e) {
+                if (tile == cluster) {
+                    wait_for_previous_kernel();
+                    steps = ext_steps(tile);
+                }
+                for (int e = (steps + 3) / 4; e > 0; --e) {
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
                     mbar_arrive(&grant[stage]);
                     advance(stage, phase);
@@ -190,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!(good = mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl))) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+                int steps = tile == cluster ? 0 : ext_steps(tile);
                 // The issue loop has to keep ahead of MMAs of 128 cycles: whole
                 // stages are unrolled, descriptors differ by an addition.
                 for (int kb = 0; kb < nk; ++kb) {
@@ -203,8 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     advance(stage, phase);
                 }
                 if (!good) break;
-                wait_for_previous_kernel();
-                for (int left = ext_steps(tile / n_col_tiles); left > 0; left -= 4) {
+                if (tile == cluster) {
+                    wait_for_previous_kernel();
+                    steps = ext_steps(tile);
+                }
+                for (int left = steps; left > 0; left -= 4) {
                     if (!(good = mbar_wait_cluster(&full[stage], phase, ctl))) break;
                     tc_fence_after_sync();
                     const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
@@ -221,118 +234,102 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
     } else if (warp < 4) {
-        // ------------------------------------------------------ announcing them
-        // A release at cluster scope waits for its thread's copies in flight, so
-        // threads without any make it, for every other stage each (with barriers
-        // of their own: each sees every phase that it has to count).
-        if (lane == 0) {
-            wait_for_previous_kernel();
-            int stage = 0, n = 0;
-            uint32_t seen = 0;  // bit s: parity of this thread's next phase of stage s
-            uint64_t* mine = written + (warp - 2) * kStages;
-            bool good = true;
-            for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
-                stage = (stage + nk) % kStages;
-                for (int e = (ext_steps(tile / n_col_tiles) + 3) / 4; e > 0; --e, ++n) {
-                    if ((n & 1) == warp - 2) {
-                        if (!(good = mbar_wait(&mine[stage], seen >> stage & 1u, ctl))) break;
-                        seen ^= 1u << stage;
-                        mbar_arrive_cluster(cluster_addr(smem_u32(&full[stage]), 0));
-                    }
-                    stage = stage + 1 == kStages ? 0 : stage + 1;
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp >= 8) {
-        // ------------------------------------------------------ adapters' stages
+        // ------------------------------------------------------ checking them
+        // Every other stage each, with barriers of their own: a warp sees every
+        // phase that it has to count.
         wait_for_previous_kernel();
-        // Two stages of copies are in flight before the first is handed on, so a
-        // tile with many adapters does not wait for each copy's latency.
-        const int row = tid - 256;  // 0..127: this CTA's token row and its W row of the tile
-        const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row * 128);
-        const auto piece_at = [&](int p) { return static_cast<uint32_t>((p ^ (row & 7)) << 4); };
-        int stage = 0, seq = 0, handed = 0;
-        uint32_t granted = 0;  // bit s: parity of grant[s]'s next phase
+        int stage = 0, n = 0, seq = 0;
+        uint32_t seen = 0;  // bit s: parity of this warp's next phase of stage s
+        uint64_t* mine = landed + (warp - 2) * kStages;
         bool good = true;
         for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
-            const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
             stage = (stage + nk) % kStages;
-            const int count = a.tile_count[mt];
-            all_of_four_warps(true);  // the last tile's list is read
-            for (int i = row; i < count; i += 128)
-                list[i] = a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + i];
-            all_of_four_warps(true);
-            const long long t = static_cast<long long>(mt) * 256 + rank * 128 + row;
-            const int id = t < a.m ? a.adapter_ids[t] : -1;
-            const int col = nt * bn + static_cast<int>(rank) * half + row;
-            const bool col_in = row < half && col < a.n;
-            const __nv_bfloat16* h_row = a.h_split + (t < a.m ? t : 0) * 2 * a.r16;
-            const __nv_bfloat16* b_row = a.B + static_cast<size_t>(col_in ? col : 0) * a.rank;
-            const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
-            const int cols = count * 2 * a.r16;
-
-            // Hands stage `st` on: its copies have landed; pieces of B that are
-            // not finite become zeros (the epilogue adds their products).
-            const auto hand_on = [&](int st) {
-                bool bad = false;
-                if (row < half) {
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        uint4* at = reinterpret_cast<uint4*>(smem + st * kStage + kHalf + row * 128 + piece_at(p));
-                        if (not_finite_bf16x8(*at)) {
-                            *at = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = (ext_steps(tile) + 3) / 4; e > 0; --e, ++n) {
+                if ((n & 1) == warp - 2) {
+                    good = __all_sync(0xffffffffu, mbar_wait(&mine[stage], seen >> stage & 1u, ctl));
+                    if (!good) break;
+                    seen ^= 1u << stage;
+                    // pieces of B that are not finite become zeros (the epilogue
+                    // adds their products)
+                    uint4* b = reinterpret_cast<uint4*>(smem + stage * kStage + kHalf) + lane;
+                    bool bad = false;
+#pragma unroll 8
+                    for (int i = 0; i < half * 8 / 32; ++i) {
+                        if (not_finite_bf16x8(b[i * 32])) {
+                            b[i * 32] = make_uint4(0u, 0u, 0u, 0u);
                             bad = true;
                         }
                     }
-                }
-                if (bad) {
-                    const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
-                    st_shared_cluster(cluster_addr(at, 0), tile + 1);
-                    st_shared_cluster(cluster_addr(at, 1), tile + 1);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&written[(handed++ & 1) * kStages + st]);
-            };
-            int ad = 0, rem = 0;       // adapter of the list and column within its 2 * r16
-            int older = -1, newer = -1;  // stages whose copies are in flight
-            for (int c0 = 0; c0 < cols; c0 += 64) {
-                good = all_of_four_warps(mbar_wait(&grant[stage], granted >> stage & 1u, ctl));
-                if (!good) break;
-                granted ^= 1u << stage;
-                const uint32_t sa = ext + static_cast<uint32_t>(stage * kStage);
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const bool in = ad < count;
-                    const int adapter = in ? list[ad] : 0;
-                    const int r = rem < a.r16 ? rem : rem - a.r16;
-                    const bool use_a = in && adapter == id, use_b = in && col_in && r < a.rank;
-                    cp_async_16(sa + piece_at(p), use_a ? h_row + rem : a.h_split, use_a ? 16u : 0u);
-                    if (row < half)
-                        cp_async_16(sa + kHalf + piece_at(p), use_b ? b_row + adapter * b_adapter + r : a.B,
-                                    use_b ? 16u : 0u);
-                    rem += 8;
-                    if (rem == 2 * a.r16) {
-                        rem = 0;
-                        ++ad;
+                    if (bad) {
+                        const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
+                        st_shared_cluster(cluster_addr(at, 0), tile + 1);
+                        st_shared_cluster(cluster_addr(at, 1), tile + 1);
+                    }
+                    fence_proxy_async_smem();  // the copies and the zeros, for the tensor core
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0)
+                            mbar_arrive(&full[stage]);
+                        else
+                            mbar_arrive_cluster(cluster_addr(smem_u32(&full[stage]), 0));
                     }
                 }
-                cp_async_commit();
-                if (older >= 0) {
-                    cp_async_wait_group<2>();
-                    hand_on(older);
+                stage = stage + 1 == kStages ? 0 : stage + 1;
+            }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------ adapters' stages
+        wait_for_previous_kernel();
+        // A thread copies piece tid % 8 of rows tid / 8 + 16 i: eight lanes take
+        // 128 contiguous bytes of a row (a row per lane would cost 32 memory
+        // transactions per instruction, 2000 cycles a stage).
+        const int pt = tid - 256, piece = pt & 7, row0 = pt >> 3;
+        const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row0 * 128 + ((piece ^ (row0 & 7)) << 4));
+        const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
+        int stage = 0, n = 0;
+        uint32_t granted = 0;  // bit s: parity of grant[s]'s next phase
+        bool good = true;
+        for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
+            const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
+            stage = (stage + nk) % kStages;
+            const int count = a.tile_count[mt];
+            // the warps go on or stop together; the last tile's list is read
+            if (!all_of_four_warps(good)) break;
+            for (int i = pt; i < count; i += 128)
+                list[i] = a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + i];
+            all_of_four_warps(true);
+            const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + row0;
+            const int col0 = nt * bn + static_cast<int>(rank) * half + row0;
+            int id[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) id[i] = t0 + 16 * i < a.m ? a.adapter_ids[t0 + 16 * i] : -1;
+            // this thread's column among the adapters': adapter of the list and
+            // column within its 2 * r16
+            int ad = piece * 8 / (2 * a.r16), rem = piece * 8 - ad * 2 * a.r16;
+            for (int c0 = 0; c0 < count * 2 * a.r16; c0 += 64, ++n) {
+                if (!(good = mbar_wait(&grant[stage], granted >> stage & 1u, ctl))) break;
+                granted ^= 1u << stage;
+                const uint32_t sa = ext + static_cast<uint32_t>(stage * kStage);
+                const bool in = ad < count;
+                const int adapter = in ? list[ad] : 0;
+                const int r = rem < a.r16 ? rem : rem - a.r16;
+                const bool b_in = in && r < a.rank;
+                const __nv_bfloat16* h = a.h_split + t0 * 2 * a.r16 + rem;
+                const __nv_bfloat16* b = a.B + adapter * b_adapter + static_cast<size_t>(col0) * a.rank + r;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool use = in && id[i] == adapter;
+                    cp_async_16(sa + i * 16 * 128, use ? h + i * 32 * a.r16 : a.h_split, use ? 16u : 0u);
                 }
-                older = newer;
-                newer = stage;
-                stage = (stage + 1) % kStages;
-            }
-            if (good && older >= 0) {
-                cp_async_wait_group<1>();
-                hand_on(older);
-            }
-            if (good && newer >= 0) {
-                cp_async_wait_group<0>();
-                hand_on(newer);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (row0 + 16 * i >= half) break;
+                    const bool use = b_in && col0 + 16 * i < a.n;
+                    cp_async_16(sa + kHalf + i * 16 * 128, use ? b + i * 16 * a.rank : a.B, use ? 16u : 0u);
+                }
+                cp_async_arrive_noinc(&landed[(n & 1) * kStages + stage]);
+                for (rem += 64; rem >= 2 * a.r16; rem -= 2 * a.r16) ++ad;
+                stage = stage + 1 == kStages ? 0 : stage + 1;
             }
         }
         cp_async_wait_all();
@@ -441,10 +438,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 // distributed shared memory.  Reads x once from HBM (16384 tokens of 2048: 11
 // us), where the projection then finds it in the L2.  Also writes the call's
 // status word and the adapters of every 256-token row tile.
-constexpr int kShrinkStages = 4;
+constexpr int kShrinkMaxStages = 10;
 constexpr int kShrinkThreads = 256;
-constexpr int kShrinkPitch = MOE_MAX_LORA_RANK + 1;
-constexpr int kShrinkSmem = kShrinkStages * kStage + 128 * kShrinkPitch * 4 + 256 + 1024;
+// Shared memory for a rank: as many stages (16 KB of x, 128 bytes per row of
+// the adapter) as fit beside the partial sums [128][r16 + 1].
+struct ShrinkSmem {
+    int stage, stages, sums, total;  // bytes, except `stages`
+};
+__host__ __device__ inline ShrinkSmem shrink_smem(int r16) {
+    ShrinkSmem s;
+    s.stage = kHalf + (r16 * 128 + 1023) / 1024 * 1024;
+    s.sums = 128 * (r16 + 1) * 4;
+    s.stages = (225280 - s.sums) / s.stage;
+    if (s.stages > kShrinkMaxStages) s.stages = kShrinkMaxStages;
+    s.total = s.stages * s.stage + s.sums + 256 + 1024;
+    return s;
+}
 
 // Distinct ids >= 0 of the first n threads' `id` (n a multiple of 32), in the
 // order of their first thread, into list; returns their number in every thread.
@@ -480,12 +489,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    float* sums = reinterpret_cast<float*>(smem + kShrinkStages * kStage);  // [128][kShrinkPitch]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sums + 128 * kShrinkPitch);
-    uint64_t* empty = full + kShrinkStages;
-    uint64_t* acc_full = empty + kShrinkStages;
+    const ShrinkSmem lay = shrink_smem(a.r16);
+    const int pitch = a.r16 + 1;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.stages * lay.stage);
+    uint64_t* empty = full + kShrinkMaxStages;
+    uint64_t* acc_full = empty + kShrinkMaxStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* sums = reinterpret_cast<float*>(smem + lay.stages * lay.stage + 256);  // [128][pitch]
     __shared__ __align__(16) int s_id[kLoraTileRows];
     __shared__ int s_list[kLoraTileRows], s_count[kLoraTileRows / 32], s_bad;
 
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     const int rank = static_cast<int>(blockIdx.x) % split, mt = static_cast<int>(blockIdx.x) / split;
     const long long t0 = static_cast<long long>(mt) * 128;
     if (tid == 0) {
-        for (int s = 0; s < kShrinkStages; ++s) {
+        for (int s = 0; s < lay.stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -553,7 +564,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0;
     const auto advance = [&] {
-        if (++stage == kShrinkStages) {
+        if (++stage == lay.stages) {
             stage = 0;
             phase ^= 1;
         }
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             if (lane == 0)
                 for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, ctl)) break;
-                    uint8_t* sa = smem + stage * kStage;
+                    uint8_t* sa = smem + stage * lay.stage;
                     mbar_arrive_expect_tx(&full[stage], bytes);
                     tma_load_2d(sa, &map_x, &full[stage], kb * 64, static_cast<int>(t0));
                     tma_load_2d(sa + kHalf, &map_a, &full[stage], kb * 64, ad * a.rank);
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                 for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!(good = mbar_wait(&full[stage], phase, ctl))) break;
                     tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4)
                         umma_bf16(tmem, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, kb > kb_lo || k4 > 0);
@@ -595,9 +606,10 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                     uint32_t v[32];
                     tmem_load_32cols(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c * 32, v);
                     tmem_load_wait();
-                    float* row = sums + ((warp & 3) * 32 + lane) * kShrinkPitch + c * 32;
+                    float* row = sums + ((warp & 3) * 32 + lane) * pitch + c * 32;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) row[i] = __uint_as_float(v[i]);
+                    for (int i = 0; i < 32; ++i)
+                        if (c * 32 + i < a.r16) row[i] = __uint_as_float(v[i]);
                 }
             tc_fence_before_sync();
             acc_phase ^= 1;
@@ -615,8 +627,12 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             if (s_id[row] != ad) continue;
             float v = 0.0f;
             if (r < a.rank) {
-                const uint32_t at = smem_u32(sums + row * kShrinkPitch + r);
-                for (int q = 0; q < split; ++q) v += split > 1 ? ld_shared_cluster(cluster_addr(at, q)) : sums[row * kShrinkPitch + r];
+                if (split > 1) {
+                    const uint32_t at = smem_u32(sums + row * pitch + r);
+                    for (int q = 0; q < split; ++q) v += ld_shared_cluster(cluster_addr(at, q));
+                } else {
+                    v = sums[row * pitch + r];
+                }
             }
             v *= scale;
             // hi + lo: 16 significant bits; a value that is not finite is its own hi part
@@ -655,20 +671,21 @@ cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x,
     static PerDeviceOnce once;
     cudaError_t err = once.run([] {
         return cudaFuncSetAttribute(lora_shrink_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kShrinkSmem);
+                                    225280 + 256 + 1024);
     });
     if (err != cudaSuccess) return err;
     // K split over as many CTAs (1 to 8, at least four stages each) as 148 SMs
-    // hold once, then adapter lanes for what is left of them
+    // hold once, then adapter lanes for what is left of them; a second lane in
+    // any case, for the tiles in which one request ends and another begins
     const long long tiles = (a.m + 127) / 128;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= 148 && (a.k + 63) / 64 >= split * 8) split *= 2;
     const long long rest = 148 / (tiles * split);
-    const unsigned lanes = static_cast<unsigned>(rest < 1 ? 1 : rest > 128 ? 128 : rest);
+    const unsigned lanes = static_cast<unsigned>(rest < 2 ? 2 : rest > 128 ? 128 : rest);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), lanes);
     cfg.blockDim = dim3(kShrinkThreads);
-    cfg.dynamicSmemBytes = kShrinkSmem;
+    cfg.dynamicSmemBytes = shrink_smem(a.r16).total;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
