@@ -185,9 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
-        if (rank == 0 && lane == 0) {
+        // The whole warp walks the loop and one elected lane issues: in a branch
+        // that only one lane enters, the compiler does not know the operands to
+        // be uniform, and the four MMAs of a stage took 489 cycles to issue.
+        if (rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
+            const bool leader = elect_one();
             // instruction descriptor: M = 256, N = bn
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                    (static_cast<uint32_t>(bn >> 3) << 17) | ((256u >> 4) << 24);
@@ -196,20 +200,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
             bool good = true;
             for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
-                if (!(good = mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl))) break;
+                good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
+                if (!good) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
                 int steps = tile == cluster ? 0 : ext_steps(tile);
-                // The issue loop has to keep ahead of MMAs of 128 cycles: whole
-                // stages are unrolled, descriptors differ by an addition.
                 for (int kb = 0; kb < nk; ++kb) {
-                    if (!(good = mbar_wait(&full[stage], phase, ctl))) break;
+                    good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
+                    if (!good) break;
                     tc_fence_after_sync();
                     const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+                    if (leader) {
 #pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4)
-                        umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
-                    umma_commit_pair(&empty[stage]);
+                        for (int k4 = 0; k4 < 4; ++k4)
+                            umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
+                        umma_commit_pair(&empty[stage]);
+                    }
+                    __syncwarp();
                     advance(stage, phase);
                 }
                 if (!good) break;
@@ -218,16 +225,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     steps = ext_steps(tile);
                 }
                 for (int left = steps; left > 0; left -= 4) {
-                    if (!(good = mbar_wait_cluster(&full[stage], phase, ctl))) break;
+                    good = __all_sync(0xffffffffu, mbar_wait_cluster(&full[stage], phase, ctl));
+                    if (!good) break;
                     tc_fence_after_sync();
                     const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
-                    for (int k4 = 0; k4 < min(4, left); ++k4)
-                        umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
-                    umma_commit_pair(&empty[stage]);
+                    if (leader) {
+                        for (int k4 = 0; k4 < min(4, left); ++k4)
+                            umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
+                        umma_commit_pair(&empty[stage]);
+                    }
+                    __syncwarp();
                     advance(stage, phase);
                 }
                 if (!good) break;
-                umma_commit_pair(&acc_full[acc]);
+                if (leader) umma_commit_pair(&acc_full[acc]);
+                __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1;
             }
