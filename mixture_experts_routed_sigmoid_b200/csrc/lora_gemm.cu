@@ -11,6 +11,10 @@
 // which are zero for the tokens of other adapters.  So they cost 2 * rank / k of
 // the projection's MMAs per adapter of a tile, and no pass over y.
 //
+// The adapters' stages have two buffers of their own beside the ring, so they
+// are copied while the projection of the same tile runs (in the ring's order
+// they came six stages ahead at most, and the tensor core waited 1.7 us a tile).
+//
 // A zero times NaN or infinity is NaN, so a piece of B that is not finite never
 // reaches the tensor core: its writer replaces it by zeros and marks the tile,
 // and the epilogue adds the piece's products for the tokens that do use it.
@@ -19,8 +23,8 @@
 // 2 and 3 check the adapters' stages and announce them to the leader, 4-7
 // epilogue, 8-11 copy the adapters' stages (cp.async: 16-byte pieces of h and B
 // picked by adapter).  A fence or a release waits for its thread's copies in
-// flight, so the threads that copy never fence: that alone took a stage from
-// 3100 cycles to its MMAs' time.  Two accumulators let the epilogue of a tile overlap
+// flight, so the threads that copy never fence (a stage took 3100 cycles when
+// they did).  Two accumulators let the epilogue of a tile overlap
 // the next tile's MMAs.  Every wait is bounded.
 #include "launch.h"
 #include "pair_mma.cuh"
@@ -28,15 +32,16 @@
 namespace moe {
 namespace {
 
-constexpr int kStages = 6;
+constexpr int kStages = 4;            // ring of the projection's stages
+constexpr int kExt = 2;               // stages of the adapters' columns, beside the ring
 constexpr int kHalf = 128 * 128;      // bytes of 128 rows x 64 columns
 constexpr int kStage = 2 * kHalf;
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
-constexpr int kFixSlots = 16;
+constexpr int kFixSlots = 4;
 constexpr int kPitch = 33;            // words of a staged epilogue row
 constexpr int kEpiBytes = 4 * 32 * kPitch * 4;
-constexpr int kSmem = kStages * kStage + kEpiBytes + 512 + kLoraTileRows * 4 + 1024;
+constexpr int kSmem = (kStages + kExt) * kStage + kEpiBytes + 512 + kLoraTileRows * 4 + 1024;
 
 __device__ __forceinline__ bool not_finite_bf16x8(const uint4& v) {
     bool bad = false;
@@ -86,30 +91,35 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStage + kEpiBytes);  // leader's are used
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (kStages + kExt) * kStage + kEpiBytes);  // leader's are used
     uint64_t* empty = full + kStages;
     uint64_t* acc_full = empty + kStages;   // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2], leader's are used
-    uint64_t* grant = acc_empty + 2;        // [kStages] an empty stage handed to the adapters' writers
-    uint64_t* landed = grant + kStages;    // [2][kStages] an adapters' stage whose copies have landed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + 2 * kStages);
+    uint64_t* ext_full = acc_empty + 2;     // [kExt], leader's are used
+    uint64_t* ext_empty = ext_full + kExt;
+    uint64_t* landed = ext_empty + kExt;    // [kExt] an adapters' stage whose copies have landed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(landed + kExt);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* bad_ext = reinterpret_cast<volatile int*>(tmem_slot + 2);  // [kExt], leader's are used
     // Tiles (1 + index) that hold a piece of B which is not finite, at the
-    // tile's place in this pair's sequence modulo kFixSlots.  The writers are
-    // at most kStages stages and two accumulators ahead of the epilogue.
-    volatile int* fix = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    // tile's place in this pair's sequence modulo kFixSlots.  The MMA issuer
+    // writes them, at most two accumulators ahead of the epilogue.
+    volatile int* fix = bad_ext + kExt;
     int* list = const_cast<int*>(fix) + kFixSlots;  // [kLoraTileRows] the tile's adapters
-    float* epi = reinterpret_cast<float*>(smem + kStages * kStage);
+    float* epi = reinterpret_cast<float*>(smem + (kStages + kExt) * kStage);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 2);   // both by the leader's copies, or one by each CTA's adapter writers
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&grant[s], 1);
-            mbar_init(&landed[s], 128);  // the copying threads
-            mbar_init(&landed[kStages + s], 128);
+        }
+        for (int s = 0; s < kExt; ++s) {
+            mbar_init(&ext_full[s], 2);   // one arrival from each CTA
+            mbar_init(&ext_empty[s], 1);
+            mbar_init(&landed[s], 128);   // the copying threads
+            bad_ext[s] = 0;
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -138,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
     // must have finished: waited for behind the first tile's projection, and
     // from the second tile on the count is loaded ahead of the tile.
-    const auto ext_steps = [&](int tile) { return a.tile_count[tile / n_col_tiles] * 2 * (a.r16 / 16); };
+    const auto ext_steps = [&](int tile) {
+        return max(a.tile_count[tile / n_col_tiles], 0) * 2 * (a.r16 / 16);
+    };
     const auto advance = [](int& stage, uint32_t& phase) {
         if (++stage == kStages) {
             stage = 0;
@@ -154,30 +166,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool good = true;
             for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
                 const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
-                int steps = tile == cluster ? 0 : ext_steps(tile);
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
                     const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
                     uint8_t* sa = smem + stage * kStage;
-                    if (rank == 0) {  // for both CTAs' copies; the stage's second arrival too
-                        mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
-                        mbar_arrive(&full[stage]);
-                    }
+                    // the leader expects both CTAs' bytes (an arrival from the other CTA
+                    // would need a release at cluster scope, 0.5 us a stage)
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
                     tma_load_2d_pair(sa, &map_x, bar, kb * 64, mt * 256 + static_cast<int>(rank) * 128);
                     tma_load_2d_pair(sa + kHalf, &map_w, bar, kb * 64, nt * bn + static_cast<int>(rank) * half);
-                    advance(stage, phase);
-                }
-                if (!good) break;
-                // This thread alone follows every phase of `empty` (a parity
-                // names a phase only to a waiter that is at most one behind);
-                // it hands the adapters' stages to their writers.
-                if (tile == cluster) {
-                    wait_for_previous_kernel();
-                    steps = ext_steps(tile);
-                }
-                for (int e = (steps + 3) / 4; e > 0; --e) {
-                    if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
-                    mbar_arrive(&grant[stage]);
                     advance(stage, phase);
                 }
             }
@@ -189,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // that only one lane enters, the compiler does not know the operands to
         // be uniform, and the four MMAs of a stage took 489 cycles to issue.
         if (rank == 0) {
-            int stage = 0, acc = 0;
+            int stage = 0, acc = 0, n = 0, seq = 0;
             uint32_t phase = 0, acc_phase = 0;
             const bool leader = elect_one();
             // instruction descriptor: M = 256, N = bn
@@ -199,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // of the ring lies below 2^18, so additions never carry out of it
             const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
             bool good = true;
-            for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
+            for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
                 good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
                 if (!good) break;
                 tc_fence_after_sync();
@@ -224,18 +221,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     wait_for_previous_kernel();
                     steps = ext_steps(tile);
                 }
-                for (int left = steps; left > 0; left -= 4) {
-                    good = __all_sync(0xffffffffu, mbar_wait_cluster(&full[stage], phase, ctl));
+                for (int left = steps; left > 0; left -= 4, ++n) {
+                    const int e = n % kExt;
+                    good = __all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl));
                     if (!good) break;
                     tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+                    const uint64_t da = desc0 + static_cast<uint64_t>((kStages + e) * (kStage >> 4));
+                    if (bad_ext[e] && lane == 0) {
+                        bad_ext[e] = 0;
+                        const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
+                        st_shared_cluster(cluster_addr(at, 0), tile + 1);
+                        st_shared_cluster(cluster_addr(at, 1), tile + 1);
+                        fence_cluster();
+                    }
+                    __syncwarp();
                     if (leader) {
                         for (int k4 = 0; k4 < min(4, left); ++k4)
                             umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
-                        umma_commit_pair(&empty[stage]);
+                        umma_commit_pair(&ext_empty[e]);
                     }
                     __syncwarp();
-                    advance(stage, phase);
                 }
                 if (!good) break;
                 if (leader) umma_commit_pair(&acc_full[acc]);
@@ -247,23 +252,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     } else if (warp < 4) {
         // ------------------------------------------------------ checking them
-        // Every other stage each, with barriers of their own: a warp sees every
-        // phase that it has to count.
+        // a stage each
         wait_for_previous_kernel();
-        int stage = 0, n = 0, seq = 0;
-        uint32_t seen = 0;  // bit s: parity of this warp's next phase of stage s
-        uint64_t* mine = landed + (warp - 2) * kStages;
+        const int e = warp - 2;
+        static_assert(kExt == 2, "one checking warp per stage");
+        uint8_t* sa = smem + (kStages + e) * kStage;
+        int n = 0;
         bool good = true;
-        for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
-            stage = (stage + nk) % kStages;
-            for (int e = (ext_steps(tile) + 3) / 4; e > 0; --e, ++n) {
-                if ((n & 1) == warp - 2) {
-                    good = __all_sync(0xffffffffu, mbar_wait(&mine[stage], seen >> stage & 1u, ctl));
+        for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
+            for (int left = ext_steps(tile); left > 0; left -= 4, ++n) {
+                if (n % kExt == e) {
+                    good = __all_sync(0xffffffffu, mbar_wait(&landed[e], n / kExt & 1u, ctl));
                     if (!good) break;
-                    seen ^= 1u << stage;
                     // pieces of B that are not finite become zeros (the epilogue
                     // adds their products)
-                    uint4* b = reinterpret_cast<uint4*>(smem + stage * kStage + kHalf) + lane;
+                    uint4* b = reinterpret_cast<uint4*>(sa + kHalf) + lane;
                     bool bad = false;
 #pragma unroll 8
                     for (int i = 0; i < half * 8 / 32; ++i) {
@@ -272,21 +275,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                             bad = true;
                         }
                     }
-                    if (bad) {
-                        const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
-                        st_shared_cluster(cluster_addr(at, 0), tile + 1);
-                        st_shared_cluster(cluster_addr(at, 1), tile + 1);
-                    }
+                    if (bad) st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(&bad_ext[e])), 0), 1);
                     fence_proxy_async_smem();  // the copies and the zeros, for the tensor core
                     __syncwarp();
                     if (lane == 0) {
                         if (rank == 0)
-                            mbar_arrive(&full[stage]);
+                            mbar_arrive(&ext_full[e]);
                         else
-                            mbar_arrive_cluster(cluster_addr(smem_u32(&full[stage]), 0));
+                            mbar_arrive_cluster(cluster_addr(smem_u32(&ext_full[e]), 0));
                     }
                 }
-                stage = stage + 1 == kStages ? 0 : stage + 1;
             }
         }
     } else if (warp >= 8) {
@@ -298,13 +296,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int pt = tid - 256, piece = pt & 7, row0 = pt >> 3;
         const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row0 * 128 + ((piece ^ (row0 & 7)) << 4));
         const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
-        int stage = 0, n = 0;
-        uint32_t granted = 0;  // bit s: parity of grant[s]'s next phase
+        int n = 0;
         bool good = true;
         for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
             const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
-            stage = (stage + nk) % kStages;
-            const int count = a.tile_count[mt];
+            const int count = max(a.tile_count[mt], 0);
             // the warps go on or stop together; the last tile's list is read
             if (!all_of_four_warps(good)) break;
             for (int i = pt; i < count; i += 128)
@@ -319,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // column within its 2 * r16
             int ad = piece * 8 / (2 * a.r16), rem = piece * 8 - ad * 2 * a.r16;
             for (int c0 = 0; c0 < count * 2 * a.r16; c0 += 64, ++n) {
-                if (!(good = mbar_wait(&grant[stage], granted >> stage & 1u, ctl))) break;
-                granted ^= 1u << stage;
-                const uint32_t sa = ext + static_cast<uint32_t>(stage * kStage);
+                const int e = n % kExt;
+                if (!(good = mbar_wait_cluster(&ext_empty[e], (n / kExt & 1u) ^ 1u, ctl))) break;
+                const uint32_t sa = ext + static_cast<uint32_t>((kStages + e) * kStage);
                 const bool in = ad < count;
                 const int adapter = in ? list[ad] : 0;
                 const int r = rem < a.r16 ? rem : rem - a.r16;
@@ -339,16 +335,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const bool use = b_in && col0 + 16 * i < a.n;
                     cp_async_16(sa + kHalf + i * 16 * 128, use ? b + i * 16 * a.rank : a.B, use ? 16u : 0u);
                 }
-                cp_async_arrive_noinc(&landed[(n & 1) * kStages + stage]);
+                cp_async_arrive_noinc(&landed[e]);
                 for (rem += 64; rem >= 2 * a.r16; rem -= 2 * a.r16) ++ad;
-                stage = stage + 1 == kStages ? 0 : stage + 1;
             }
         }
         cp_async_wait_all();
     } else if (warp >= 4) {
         // ------------------------------------------------------ epilogue
         wait_for_previous_kernel();
-        const bool write = *a.status == kDevOk;
+        // an adapter id out of range anywhere in the call: nothing is written
+        bool bad = false;
+        for (int i = lane; i < n_tiles / n_col_tiles; i += 32) bad |= a.tile_count[i] < 0;
+        const bool write = !__any_sync(0xffffffffu, bad);
+        if (!write && blockIdx.x == 0 && tid == 128) set_status(a.status, kDevBadId);
         const int quarter = warp & 3;
         float* buf = epi + quarter * 32 * kPitch;
         int acc = 0, seq = 0;
@@ -448,8 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 // tiles x cluster, adapter lanes): lane j of L takes every L-th adapter of its
 // tokens, the CTAs of a cluster split K and add their sums in rank order over
 // distributed shared memory.  Reads x once from HBM (16384 tokens of 2048: 11
-// us), where the projection then finds it in the L2.  Also writes the call's
-// status word and the adapters of every 256-token row tile.
+// us), where the projection then finds it in the L2.  Also writes the adapters
+// of every 256-token row tile (their number is -1 where an id is out of range).
 constexpr int kShrinkMaxStages = 10;
 constexpr int kShrinkThreads = 256;
 // Shared memory for a rank: as many stages (16 KB of x, 128 bytes per row of
@@ -540,30 +539,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 
     const auto id_of = [&](long long t) {
         const int id = t < a.m ? a.adapter_ids[t] : -1;
-        return id < a.n_adapters ? id : -1;  // out of range: reported below, no adapter is read for it
+        if (id < -1 || id >= a.n_adapters) s_bad = 1;  // of the 256 tokens from t0 on
+        return id < a.n_adapters ? id : -1;            // no adapter is read for it
     };
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-        bool bad = false;
-        const auto check = [&](int id) { bad |= id < -1 || id >= a.n_adapters; };
-        const int* ids = a.adapter_ids;
-        const long long vec = reinterpret_cast<uintptr_t>(ids) % 16 ? 0 : a.m / 4;
-#pragma unroll 8
-        for (long long i = tid; i < vec; i += kShrinkThreads) {
-            const int4 v = reinterpret_cast<const int4*>(ids)[i];
-            check(v.x);
-            check(v.y);
-            check(v.z);
-            check(v.w);
-        }
-        for (long long t = vec * 4 + tid; t < a.m; t += kShrinkThreads) check(ids[t]);
-        if (bad) s_bad = 1;
-        __syncthreads();
-        if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
-    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *a.status = kDevOk;
     if (blockIdx.y == 0 && rank == 0 && mt % 2 == 0) {
         const int n = distinct_ids(id_of(t0 + tid), kLoraTileRows, s_id, s_count,
                                    a.tile_list + static_cast<size_t>(mt / 2) * kLoraTileRows);
-        if (tid == 0) a.tile_count[mt / 2] = n;
+        if (tid == 0) a.tile_count[mt / 2] = s_bad ? -1 : n;  // an id out of range in the tile
     }
     const int my_id = tid < 128 ? id_of(t0 + tid) : -1;
     const int n_list = distinct_ids(my_id, 128, s_id, s_count, s_list);  // s_id: the tile's ids
@@ -595,21 +578,25 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                     advance();
                 }
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-                bool good = true;
-                for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                    if (!(good = mbar_wait(&full[stage], phase, ctl))) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
+            const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+            const bool leader = elect_one();
+            bool good = true;
+            for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
+                if (!good) break;
+                tc_fence_after_sync();
+                const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
+                if (leader) {
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4)
                         umma_bf16(tmem, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, kb > kb_lo || k4 > 0);
                     umma_commit(&empty[stage]);
-                    advance();
                 }
-                if (good) umma_commit(acc_full);
+                __syncwarp();
+                advance();
             }
+            if (good && leader) umma_commit(acc_full);
+            __syncwarp();
         } else if (warp >= 4) {
             const bool good = __all_sync(0xffffffffu, mbar_wait(acc_full, acc_phase, ctl));
             tc_fence_after_sync();
