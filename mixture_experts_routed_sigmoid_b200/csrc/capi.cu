@@ -928,21 +928,32 @@ int lora_k_splits(long long m, int k, int rank) {
     return s < 1 ? 1 : s > 8 ? 8 : static_cast<int>(s);
 }
 
-// Columns of a GEMM tile (a multiple of 32, at most 256): the width whose
-// tiles (256 tokens high, one per CTA pair at a time) take the least time.  A
-// stage of 64 columns of K costs the larger of its MMAs (2 cycles per column)
-// and its copies (16 KB + 64 bytes per column and CTA, at about 80 bytes a
-// cycle).
-int lora_tile_columns(long long m, int n) {
-    int pick = 256;
-    double best = 0;
-    for (int bn = 256; bn >= 64; bn -= 32) {
-        const long long tiles = (m + 255) / 256 * ((n + bn - 1) / bn);
-        const double stage = 2.0 * bn > 205 + 0.8 * bn ? 2.0 * bn : 205 + 0.8 * bn;
-        const double cost = static_cast<double>((tiles + 73) / 74) * stage;
-        if (bn == 256 || cost < best) {
-            best = cost;
-            pick = bn;
+// Columns of a GEMM tile (a multiple of 32, at most 256) and the CTA pairs that
+// share its K (1, 2 or 4): those whose tiles (256 tokens high) take the least
+// time.  A stage of 64 columns of K takes 2 cycles per column for its MMAs, but
+// at least 365 to issue; a tile costs about 4 stages on top, and joining the
+// parts of a split one about 3000 + 10 per column.  A split tile is one
+// cluster of 4 or 8 CTAs, of which 32 or 16 fit on the GPU at once.
+// (Measured at 4096 x 4096 x 4096: 192 columns 92 us, 256 columns 99.)
+struct LoraTile {
+    int columns, split;
+};
+
+LoraTile lora_tile(long long m, int n, int k) {
+    LoraTile pick{256, 1};
+    long long best = -1;
+    const long long nk = (k + 63) / 64;
+    for (int split = 1; split <= 4 && nk >= 4 * split; split *= 2) {
+        const long long at_once = split == 1 ? 74 : 64 / split;
+        for (int bn = 256; bn >= 64; bn -= 32) {
+            const long long tiles = (m + 255) / 256 * ((n + bn - 1) / bn);
+            const long long stage = 2 * bn > 365 ? 2 * bn : 365;
+            const long long join = split > 1 ? 3000 + 10 * bn : 0;
+            const long long cost = (tiles + at_once - 1) / at_once * (stage * ((nk + split - 1) / split + 4) + join);
+            if (best < 0 || cost <= best) {
+                best = cost;
+                pick = LoraTile{bn, split};
+            }
         }
     }
     return pick;
@@ -1048,20 +1059,20 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.y_dtype = y_dtype;
     a.r16 = L.r16;
     a.wait_limit_ns = moe::kDefaultWaitLimitNs;
-    const int bn = stream_w ? 0 : lora_tile_columns(m, n);
     cudaError_t err;
     if (stream_w) {
         err = moe::launch_lora_shrink(a, s);
         if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
         err = moe::launch_lora_stream(a, num_sms(), s);
     } else {
+        const LoraTile tile = lora_tile(m, n, k);
         CUtensorMap map_x, map_w, map_a;
         MOE_TRY(make_map(&map_x, x, k, m, 128, "x"));
-        MOE_TRY(make_map(&map_w, W, k, n, bn / 2, "W"));
+        MOE_TRY(make_map(&map_w, W, k, n, tile.columns / 2, "W"));
         MOE_TRY(make_map(&map_a, A, k, static_cast<unsigned long long>(n_adapters) * rank, rank, "A"));
         err = moe::launch_lora_shrink_gemm(a, map_x, map_a, s);
         if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
-        err = moe::launch_lora_gemm(a, map_x, map_w, bn, num_sms(), s);
+        err = moe::launch_lora_gemm(a, map_x, map_w, tile.columns, tile.split, num_sms(), s);
     }
     if (err != cudaSuccess) return cuda_fail(err, "projection launch");
     return ok();

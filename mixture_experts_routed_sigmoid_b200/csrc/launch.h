@@ -224,9 +224,10 @@ cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stre
 // map_x: boxes of 128 rows; map_a: of `rank` rows of [n_adapters * rank, k].
 cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_a,
                                     cudaStream_t stream);
-// map_x: boxes of 128 rows, map_w: boxes of bn / 2 rows (64 columns each).
+// map_x: boxes of 128 rows, map_w: boxes of bn / 2 rows (64 columns each);
+// split: CTA pairs that share a tile's K (1, 2 or 4).
 cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
-                             int num_sms, cudaStream_t stream);
+                             int split, int num_sms, cudaStream_t stream);
 
 // Sets the calling thread's moe_last_error() message.
 void set_last_error(const char* msg);

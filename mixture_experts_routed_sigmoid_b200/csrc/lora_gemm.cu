@@ -11,6 +11,11 @@
 // which are zero for the tokens of other adapters.  So they cost 2 * rank / k of
 // the projection's MMAs per adapter of a tile, and no pass over y.
 //
+// Where there are fewer tiles than CTA pairs, a cluster of 2 or 4 pairs shares
+// a tile (SPLIT): each pair takes a part of K and of the adapters' stages, the
+// partial tiles meet in distributed shared memory, and every CTA adds and
+// stores its share of the columns, pairs in order.
+//
 // The adapters' stages have two buffers of their own beside the ring, so they
 // are copied while the projection of the same tile runs (in the ring's order
 // they came six stages ahead at most, and the tensor core waited 1.7 us a tile).
@@ -32,16 +37,24 @@
 namespace moe {
 namespace {
 
-constexpr int kStages = 4;            // ring of the projection's stages
+constexpr int kMaxStages = 8;         // ring of the projection's stages
 constexpr int kExt = 2;               // stages of the adapters' columns, beside the ring
 constexpr int kHalf = 128 * 128;      // bytes of 128 rows x 64 columns
-constexpr int kStage = 2 * kHalf;
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr int kFixSlots = 4;
+constexpr int kPartPitch = 36;        // words of a partial tile's row of 32 columns
 constexpr int kPitch = 33;            // words of a staged epilogue row
 constexpr int kEpiBytes = 4 * 32 * kPitch * 4;
-constexpr int kSmem = (kStages + kExt) * kStage + kEpiBytes + 512 + kLoraTileRows * 4 + 1024;
+constexpr int kTail = kEpiBytes + 512 + kLoraTileRows * 4 + 1024;  // behind the stages, and alignment
+constexpr int kSmemLimit = 232448;
+// Bytes of a stage and the ring's stages for tiles of bn columns: 4 at 256, 5
+// at 192 (430 -> 385 cycles a stage against 4 there), 8 at 64.
+__host__ __device__ inline int stage_bytes(int bn) { return kHalf + bn / 2 * 128; }
+__host__ __device__ inline int ring_stages(int bn) {
+    const int fit = (kSmemLimit - kTail) / stage_bytes(bn) - kExt;
+    return fit < kMaxStages ? fit : kMaxStages;
+}
 
 __device__ __forceinline__ bool not_finite_bf16x8(const uint4& v) {
     bool bad = false;
@@ -85,15 +98,64 @@ __device__ __noinline__ float fix_up(const LoraArgs& a, long long t, int id, int
     return s;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+// Stores 32 rows x 32 columns from shared memory (rows of kPitch words).
+__device__ __forceinline__ void store_chunk(const LoraArgs& a, const float* buf, long long t0, int col0,
+                                            int lane) {
+    if (a.y_dtype == MOE_DTYPE_BF16) {
+        // 8 columns per lane: 8 rows x 64 bytes per instruction
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
+        const int cc = (lane & 3) * 8, col = col0 + cc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (t0 + r >= a.m || col >= a.n) continue;
+            const float* s = buf + r * kPitch + cc;
+            __nv_bfloat16* dst = y + (t0 + r) * a.n + col;
+            if ((a.n & 7) == 0) {
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * q], s[2 * q + 1]);
+                    o[q] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                for (int q = 0; q < 8; ++q)
+                    if (col + q < a.n) dst[q] = __float2bfloat16_rn(s[q]);
+            }
+        }
+    } else {
+        float* y = static_cast<float*>(a.y);
+        const int cc = (lane & 7) * 4, col = col0 + cc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (t0 + r >= a.m || col >= a.n) continue;
+            const float* s = buf + r * kPitch + cc;
+            float* dst = y + (t0 + r) * a.n + col;
+            if ((a.n & 3) == 0) {
+                *reinterpret_cast<float4*>(dst) = make_float4(s[0], s[1], s[2], s[3]);
+            } else {
+                for (int q = 0; q < 4; ++q)
+                    if (col + q < a.n) dst[q] = s[q];
+            }
+        }
+    }
+}
+
+// grid: CTA pairs as clusters of 2 that walk the tiles, or with SPLIT a cluster
+// of `split` pairs per tile.
+template <bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
     lora_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                     const LoraArgs a, int bn, int n_col_tiles, int n_tiles) {
+                     const LoraArgs a, int bn, int n_col_tiles, int n_tiles, int split) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (kStages + kExt) * kStage + kEpiBytes);  // leader's are used
-    uint64_t* empty = full + kStages;
-    uint64_t* acc_full = empty + kStages;   // [2]
+    const int stage_size = stage_bytes(bn), n_stages = ring_stages(bn);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (n_stages + kExt) * stage_size + kEpiBytes);  // leader's are used
+    uint64_t* empty = full + kMaxStages;
+    uint64_t* acc_full = empty + kMaxStages;   // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2], leader's are used
     uint64_t* ext_full = acc_empty + 2;     // [kExt], leader's are used
     uint64_t* ext_empty = ext_full + kExt;
@@ -106,12 +168,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // writes them, at most two accumulators ahead of the epilogue.
     volatile int* fix = bad_ext + kExt;
     int* list = const_cast<int*>(fix) + kFixSlots;  // [kLoraTileRows] the tile's adapters
-    float* epi = reinterpret_cast<float*>(smem + (kStages + kExt) * kStage);
+    float* epi = reinterpret_cast<float*>(smem + (n_stages + kExt) * stage_size);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_rank();
+    // this CTA of its pair, the pair's leader, and the pair's part of a split tile
+    const uint32_t rank = cluster_rank() & 1u, lead = cluster_rank() & ~1u;
+    const int part = SPLIT ? static_cast<int>(cluster_rank() >> 1) : 0, parts = SPLIT ? split : 1;
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < n_stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -142,21 +206,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, a.status, a.wait_limit_ns};
 
-    const int cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
-    const int nk = (a.k + 63) / 64;
+    const int cluster = blockIdx.x / (2 * parts), n_clusters = gridDim.x / (2 * parts);
+    const int nk_all = (a.k + 63) / 64, kb_lo = nk_all * part / parts;
+    const int nk = nk_all * (part + 1) / parts - kb_lo;  // this pair's stages of the projection
     const int half = bn / 2;
     // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
     // must have finished: waited for behind the first tile's projection, and
     // from the second tile on the count is loaded ahead of the tile.
-    const auto ext_steps = [&](int tile) {
-        return max(a.tile_count[tile / n_col_tiles], 0) * 2 * (a.r16 / 16);
+    const auto ext_steps = [&](int tile, int& first) {
+        const int all = max(a.tile_count[tile / n_col_tiles], 0) * 2 * (a.r16 / 16);
+        if (!SPLIT) {
+            first = 0;
+            return all;
+        }
+        const int stages = (all + 3) / 4;  // whole stages to each pair
+        first = stages * part / parts * 4;
+        return min(stages * (part + 1) / parts * 4, all) - first;
     };
-    const auto advance = [](int& stage, uint32_t& phase) {
-        if (++stage == kStages) {
+    const auto advance = [&](int& stage, uint32_t& phase) {
+        if (++stage == n_stages) {
             stage = 0;
             phase ^= 1;
         }
     };
+
+    bool write = false;  // (epilogue) no id is out of range
+    // SPLIT: the pair's partial tile [bn / 32][128 rows][kPartPitch], over the
+    // stages once they are used up
+    float* partial = reinterpret_cast<float*>(smem);
 
     if (warp == 0) {
         // ------------------------------------------------------ tile copies
@@ -168,13 +245,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
-                    const uint32_t bar = cluster_addr(smem_u32(&full[stage]), 0);
-                    uint8_t* sa = smem + stage * kStage;
+                    const uint32_t bar = cluster_addr(smem_u32(&full[stage]), lead);
+                    uint8_t* sa = smem + stage * stage_size;
                     // the leader expects both CTAs' bytes (an arrival from the other CTA
                     // would need a release at cluster scope, 0.5 us a stage)
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
-                    tma_load_2d_pair(sa, &map_x, bar, kb * 64, mt * 256 + static_cast<int>(rank) * 128);
-                    tma_load_2d_pair(sa + kHalf, &map_w, bar, kb * 64, nt * bn + static_cast<int>(rank) * half);
+                    tma_load_2d_pair(sa, &map_x, bar, (kb_lo + kb) * 64, mt * 256 + static_cast<int>(rank) * 128);
+                    tma_load_2d_pair(sa + kHalf, &map_w, bar, (kb_lo + kb) * 64, nt * bn + static_cast<int>(rank) * half);
                     advance(stage, phase);
                 }
             }
@@ -201,17 +278,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!good) break;
                 tc_fence_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-                int steps = tile == cluster ? 0 : ext_steps(tile);
+                int first, steps = tile == cluster ? 0 : ext_steps(tile, first);
                 for (int kb = 0; kb < nk; ++kb) {
                     good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
                     if (!good) break;
                     tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (kStage >> 4));
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
                     if (leader) {
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4)
                             umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
-                        umma_commit_pair(&empty[stage]);
+                        umma_commit_pair(&empty[stage], lead);
                     }
                     __syncwarp();
                     advance(stage, phase);
@@ -219,31 +296,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!good) break;
                 if (tile == cluster) {
                     wait_for_previous_kernel();
-                    steps = ext_steps(tile);
+                    steps = ext_steps(tile, first);
                 }
                 for (int left = steps; left > 0; left -= 4, ++n) {
                     const int e = n % kExt;
                     good = __all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl));
                     if (!good) break;
                     tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>((kStages + e) * (kStage >> 4));
+                    const uint64_t da = desc0 + static_cast<uint64_t>((n_stages + e) * (stage_size >> 4));
                     if (bad_ext[e] && lane == 0) {
                         bad_ext[e] = 0;
                         const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
-                        st_shared_cluster(cluster_addr(at, 0), tile + 1);
-                        st_shared_cluster(cluster_addr(at, 1), tile + 1);
+                        for (int q = 0; q < 2 * parts; ++q) st_shared_cluster(cluster_addr(at, q), tile + 1);
                         fence_cluster();
                     }
                     __syncwarp();
                     if (leader) {
                         for (int k4 = 0; k4 < min(4, left); ++k4)
                             umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
-                        umma_commit_pair(&ext_empty[e]);
+                        umma_commit_pair(&ext_empty[e], lead);
                     }
                     __syncwarp();
                 }
                 if (!good) break;
-                if (leader) umma_commit_pair(&acc_full[acc]);
+                if (leader) umma_commit_pair(&acc_full[acc], lead);
                 __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1;
@@ -256,11 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         wait_for_previous_kernel();
         const int e = warp - 2;
         static_assert(kExt == 2, "one checking warp per stage");
-        uint8_t* sa = smem + (kStages + e) * kStage;
+        uint8_t* sa = smem + (n_stages + e) * stage_size;
         int n = 0;
         bool good = true;
         for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
-            for (int left = ext_steps(tile); left > 0; left -= 4, ++n) {
+            int first;
+            for (int left = ext_steps(tile, first); left > 0; left -= 4, ++n) {
                 if (n % kExt == e) {
                     good = __all_sync(0xffffffffu, mbar_wait(&landed[e], n / kExt & 1u, ctl));
                     if (!good) break;
@@ -275,14 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                             bad = true;
                         }
                     }
-                    if (bad) st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(&bad_ext[e])), 0), 1);
+                    if (bad) st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(&bad_ext[e])), lead), 1);
                     fence_proxy_async_smem();  // the copies and the zeros, for the tensor core
                     __syncwarp();
                     if (lane == 0) {
                         if (rank == 0)
                             mbar_arrive(&ext_full[e]);
                         else
-                            mbar_arrive_cluster(cluster_addr(smem_u32(&ext_full[e]), 0));
+                            mbar_arrive_cluster(cluster_addr(smem_u32(&ext_full[e]), lead));
                     }
                 }
             }
@@ -313,11 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int i = 0; i < 8; ++i) id[i] = t0 + 16 * i < a.m ? a.adapter_ids[t0 + 16 * i] : -1;
             // this thread's column among the adapters': adapter of the list and
             // column within its 2 * r16
-            int ad = piece * 8 / (2 * a.r16), rem = piece * 8 - ad * 2 * a.r16;
-            for (int c0 = 0; c0 < count * 2 * a.r16; c0 += 64, ++n) {
+            int first;
+            const int steps = ext_steps(tile, first);
+            int ad = (first * 16 + piece * 8) / (2 * a.r16), rem = first * 16 + piece * 8 - ad * 2 * a.r16;
+            for (int left = steps; left > 0; left -= 4, ++n) {
                 const int e = n % kExt;
                 if (!(good = mbar_wait_cluster(&ext_empty[e], (n / kExt & 1u) ^ 1u, ctl))) break;
-                const uint32_t sa = ext + static_cast<uint32_t>((kStages + e) * kStage);
+                const uint32_t sa = ext + static_cast<uint32_t>((n_stages + e) * stage_size);
                 const bool in = ad < count;
                 const int adapter = in ? list[ad] : 0;
                 const int r = rem < a.r16 ? rem : rem - a.r16;
@@ -346,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         // an adapter id out of range anywhere in the call: nothing is written
         bool bad = false;
         for (int i = lane; i < n_tiles / n_col_tiles; i += 32) bad |= a.tile_count[i] < 0;
-        const bool write = !__any_sync(0xffffffffu, bad);
+        write = !__any_sync(0xffffffffu, bad);
         if (!write && blockIdx.x == 0 && tid == 128) set_status(a.status, kDevBadId);
         const int quarter = warp & 3;
         float* buf = epi + quarter * 32 * kPitch;
@@ -359,6 +438,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + quarter * 32;
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                    static_cast<uint32_t>(acc * 256);
+            if (SPLIT) {  // this pair's partial tile, for the whole cluster
+#pragma unroll 1
+                for (int c = 0; c < bn / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_load_32cols(taddr + c * 32, v);
+                    tmem_load_wait();
+                    float4* dst = reinterpret_cast<float4*>(partial + (c * 128 + quarter * 32 + lane) * kPartPitch);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        dst[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                }
+                break;
+            }
             const bool mend = write && fix[seq % kFixSlots] == tile + 1;
             const int id = mend && t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
 #pragma unroll 1
@@ -375,53 +468,67 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) buf[lane * kPitch + j] = __uint_as_float(v[j]);
                 __syncwarp();
-                if (a.y_dtype == MOE_DTYPE_BF16) {
-                    // 8 columns per lane: 8 rows x 64 bytes per instruction
-                    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
-                    const int cc = (lane & 3) * 8, col = col0 + cc;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = i * 8 + (lane >> 2);
-                        if (!write || t0 + r >= a.m || col >= a.n) continue;
-                        const float* s = buf + r * kPitch + cc;
-                        __nv_bfloat16* dst = y + (t0 + r) * a.n + col;
-                        if ((a.n & 7) == 0) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * q], s[2 * q + 1]);
-                                o[q] = *reinterpret_cast<const uint32_t*>(&b);
-                            }
-                            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-                        } else {
-                            for (int q = 0; q < 8; ++q)
-                                if (col + q < a.n) dst[q] = __float2bfloat16_rn(s[q]);
-                        }
-                    }
-                } else {
-                    float* y = static_cast<float*>(a.y);
-                    const int cc = (lane & 7) * 4, col = col0 + cc;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + (lane >> 3);
-                        if (!write || t0 + r >= a.m || col >= a.n) continue;
-                        const float* s = buf + r * kPitch + cc;
-                        float* dst = y + (t0 + r) * a.n + col;
-                        if ((a.n & 3) == 0) {
-                            *reinterpret_cast<float4*>(dst) = make_float4(s[0], s[1], s[2], s[3]);
-                        } else {
-                            for (int q = 0; q < 4; ++q)
-                                if (col + q < a.n) dst[q] = s[q];
-                        }
-                    }
-                }
+                if (write) store_chunk(a, buf, t0, col0, lane);
                 __syncwarp();
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[acc]), 0));
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[acc]), lead));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1;
+        }
+    }
+    if (SPLIT) {
+        __syncwarp();
+        tc_fence_before_sync();
+        __syncthreads();
+        cluster_sync();
+        if (warp >= 4 && warp < 8 && write) {
+            // columns 32 c of the tile, c = part, part + parts, ...: all pairs'
+            // partial sums, in their order
+            const int quarter = warp & 3, tile = cluster;
+            const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
+            const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + quarter * 32;
+            const bool mend = fix[0] == tile + 1;
+            const int id = mend && t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
+            float* buf = epi + quarter * 32 * kPitch;
+#pragma unroll 1
+            for (int c = part; c < bn / 32; c += parts) {
+                const int col0 = nt * bn + c * 32;
+                if (col0 >= a.n) break;
+                const uint32_t at = smem_u32(partial + (c * 128 + quarter * 32 + (lane >> 3)) * kPartPitch + (lane & 7) * 4);
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = ld_shared_cluster_f4(cluster_addr(at + i * 16 * kPartPitch, rank));
+                for (int q = 1; q < parts; ++q) {
+                    float4 u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        u[i] = ld_shared_cluster_f4(cluster_addr(at + i * 16 * kPartPitch, 2 * q + rank));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        v[i].x += u[i].x;
+                        v[i].y += u[i].y;
+                        v[i].z += u[i].z;
+                        v[i].w += u[i].w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float* dst = buf + (i * 4 + (lane >> 3)) * kPitch + (lane & 7) * 4;
+                    dst[0] = v[i].x;
+                    dst[1] = v[i].y;
+                    dst[2] = v[i].z;
+                    dst[3] = v[i].w;
+                }
+                __syncwarp();
+                if (id >= 0)
+                    for (int j = 0; j < 32; ++j)
+                        if (col0 + j < a.n) buf[lane * kPitch + j] += fix_up(a, t0 + lane, id, col0 + j);
+                __syncwarp();
+                store_chunk(a, buf, t0, col0, lane);
+                __syncwarp();
+            }
         }
     }
     // A CTA that gave up may have copies or MMAs in flight: let them land.
@@ -621,25 +728,44 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         // this CTA's rows of the tile: the partial sums of all CTAs, in rank order
         const float scale = a.scales ? a.scales[ad] : 1.0f;
         const int r_lo = 128 * rank / split, r_hi = 128 * (rank + 1) / split;
-        for (int u = tid; u < (r_hi - r_lo) * a.r16; u += kShrinkThreads) {
-            const int row = r_lo + u / a.r16, r = u % a.r16;
+        for (int row = r_lo + warp; row < r_hi; row += kShrinkThreads / 32) {
             if (s_id[row] != ad) continue;
-            float v = 0.0f;
-            if (r < a.rank) {
-                if (split > 1) {
-                    const uint32_t at = smem_u32(sums + row * pitch + r);
-                    for (int q = 0; q < split; ++q) v += ld_shared_cluster(cluster_addr(at, q));
-                } else {
-                    v = sums[row * pitch + r];
+            for (int r = 2 * lane; r < a.r16; r += 64) {  // a pair of columns per lane
+                float v[2] = {0.0f, 0.0f};
+                if (r < a.rank) {  // even, as the rank is
+                    const float* own = sums + row * pitch + r;
+                    if (split > 1) {
+                        const uint32_t at = smem_u32(own);
+                        for (int q = 0; q < split; ++q) {
+                            const uint32_t there = cluster_addr(at, q);
+                            v[0] += ld_shared_cluster(there);
+                            v[1] += ld_shared_cluster(there + 4);
+                        }
+                    } else {
+                        v[0] = own[0];
+                        v[1] = own[1];
+                    }
                 }
+                // hi + lo: 16 significant bits; a value that is not finite is its own hi part
+                __nv_bfloat162 hi, lo;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float x = v[i] * scale;
+                    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+                    const float hf = __bfloat162float(h);
+                    const __nv_bfloat16 l = __float2bfloat16_rn(fabsf(hf) <= 3.4e38f ? x - hf : 0.0f);
+                    if (i == 0) {
+                        hi.x = h;
+                        lo.x = l;
+                    } else {
+                        hi.y = h;
+                        lo.y = l;
+                    }
+                }
+                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.h_split + (t0 + row) * 2 * a.r16 + r);
+                dst[0] = hi;
+                dst[a.r16 / 2] = lo;
             }
-            v *= scale;
-            // hi + lo: 16 significant bits; a value that is not finite is its own hi part
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            const float hf = __bfloat162float(hi);
-            __nv_bfloat16* dst = a.h_split + (t0 + row) * 2 * a.r16 + r;
-            dst[0] = hi;
-            dst[a.r16] = __float2bfloat16_rn(fabsf(hf) <= 3.4e38f ? v - hf : 0.0f);
         }
         // the sums are read; the accumulator is free
         if (split > 1)
@@ -696,27 +822,39 @@ cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x,
     return cudaLaunchKernelEx(&cfg, lora_shrink_gemm_kernel, map_x, map_a, a, split);
 }
 
-cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
-                             int num_sms, cudaStream_t stream) {
+template <bool SPLIT>
+static cudaError_t launch_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
+                               int split, int num_sms, cudaStream_t stream) {
     static PerDeviceOnce once;
     cudaError_t err = once.run([] {
-        return cudaFuncSetAttribute(lora_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        return cudaFuncSetAttribute(lora_gemm_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemLimit);
     });
     if (err != cudaSuccess) return err;
     const long long n_col = (a.n + bn - 1) / bn, tiles = (a.m + 255) / 256 * n_col;
-    const long long pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+    const long long clusters = SPLIT || tiles < num_sms / 2 ? tiles : num_sms / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * split * clusters));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = (ring_stages(bn) + kExt) * stage_bytes(bn) + kTail;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2 * split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_gemm_kernel, map_x, map_w, a, bn, static_cast<int>(n_col),
-                              static_cast<int>(tiles));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, lora_gemm_kernel<SPLIT>, map_x, map_w, a, bn, static_cast<int>(n_col),
+                              static_cast<int>(tiles), split);
+}
+
+cudaError_t launch_lora_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_w, int bn,
+                             int split, int num_sms, cudaStream_t stream) {
+    return split > 1 ? launch_gemm<true>(a, map_x, map_w, bn, split, num_sms, stream)
+                     : launch_gemm<false>(a, map_x, map_w, bn, 1, num_sms, stream);
 }
 
 }  // namespace moe

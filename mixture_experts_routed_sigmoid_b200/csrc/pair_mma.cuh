@@ -41,6 +41,15 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void st_shared_cluster(uint32_t addr, int v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -112,12 +121,13 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
-// Arrives once on `bar` of both CTAs when the MMAs issued so far have finished.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrives once on `bar` of both CTAs (cluster ranks `lead` and lead + 1) when
+// the MMAs issued so far have finished.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t lead) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3u << lead))
         : "memory");
 }
 
