@@ -933,7 +933,8 @@ int lora_k_splits(long long m, int k, int rank) {
 // time.  A stage of 64 columns of K takes 2 cycles per column for its MMAs, but
 // at least 365 to issue; a tile costs about 4 stages on top, and joining the
 // parts of a split one about 3000 + 10 per column.  A split tile is one
-// cluster of 4 or 8 CTAs, of which 32 or 16 fit on the GPU at once.
+// cluster of 4 or 8 CTAs, of which 33 or 15 fit on the GPU at once (the
+// occupancy query's answer).
 // (Measured at 4096 x 4096 x 4096: 192 columns 92 us, 256 columns 99.)
 struct LoraTile {
     int columns, split;
@@ -944,7 +945,7 @@ LoraTile lora_tile(long long m, int n, int k) {
     long long best = -1;
     const long long nk = (k + 63) / 64;
     for (int split = 1; split <= 4 && nk >= 4 * split; split *= 2) {
-        const long long at_once = split == 1 ? 74 : 64 / split;
+        const long long at_once = split == 1 ? 74 : split == 2 ? 33 : 15;
         for (int bn = 256; bn >= 64; bn -= 32) {
             const long long tiles = (m + 255) / 256 * ((n + bn - 1) / bn);
             const long long stage = 2 * bn > 365 ? 2 * bn : 365;

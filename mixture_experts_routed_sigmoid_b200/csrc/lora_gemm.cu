@@ -279,19 +279,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
                 int first, steps = tile == cluster ? 0 : ext_steps(tile, first);
+                bool ready = false;
                 for (int kb = 0; kb < nk; ++kb) {
-                    good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
+                    good = __all_sync(0xffffffffu, ready || mbar_wait(&full[stage], phase, ctl));
                     if (!good) break;
                     tc_fence_after_sync();
                     const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
+                    uint64_t* done = &empty[stage];
+                    advance(stage, phase);
+                    // the next stage's barrier is asked while these MMAs are issued
+                    if (kb + 1 < nk) ready = mbar_test(&full[stage], phase);
                     if (leader) {
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4)
                             umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
-                        umma_commit_pair(&empty[stage], lead);
+                        umma_commit_pair(done, lead);
                     }
                     __syncwarp();
-                    advance(stage, phase);
                 }
                 if (!good) break;
                 if (tile == cluster) {
