@@ -3,13 +3,13 @@
 //   y[t] = W x[t] + scales[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
 // (a = -1: the projection alone).
 //
-// Kernel 1 (shrink), m <= 64: h[t] = A[a] x[t].  An item is 32 consecutive tokens and
+// Kernel 1 (shrink), m <= 32: h[t] = A[a] x[t].  An item is 32 consecutive tokens and
 //   one of the adapters that occur among them; only those tokens' rows of x
 //   are read.  The tokens are the rows of the MMA (stream_mma.cuh, with x in
 //   the place of the weights), the adapter's rank its columns; rows of other
 //   tokens are dropped by selection, never by a multiplication with zero, so
 //   an adapter that holds NaN or infinities reaches its own requests only.
-// Kernel 2, m <= 64: streams W once through mma.sync (stream_mma.cuh) and
+// Kernel 2, m <= 32: streams W once through mma.sync (stream_mma.cuh) and
 //   adds scales[a] * B[a] h in its epilogue.
 // Larger m: the two tcgen05 kernels of lora_gemm.cu.
 #include "launch.h"
@@ -40,28 +40,13 @@ template <int NT>  // NT: groups of 8 rank rows per item
 __global__ void __launch_bounds__(kThreads, 1)
     lora_shrink_kernel(const LoraArgs a, int rank_tiles, int ks) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    __shared__ int s_bad;
     allow_next_kernel();  // it waits for this one's writes before it reads them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
-        // the call's status word: any adapter id outside [-1, n_adapters)
-        if (tid == 0) s_bad = 0;
-        __syncthreads();
-        bool bad = false;
-#pragma unroll 8
-        for (long long t = tid; t < a.m; t += kThreads) {
-            const int id = a.adapter_ids[t];
-            bad |= id < -1 || id >= a.n_adapters;
-        }
-        if (bad) s_bad = 1;
-        __syncthreads();
-        if (tid == 0) *a.status = s_bad ? kDevBadId : kDevOk;
-    }
     const int item = warp / ks, part = warp % ks;  // this warp's tokens and its share of K
     const long long t0 = static_cast<long long>(blockIdx.x) * (kWarps / ks * kGroup) + item * kGroup;
     int my_id = t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
-    if (my_id >= a.n_adapters) my_id = -1;  // reported above; no adapter is read for it
+    if (my_id >= a.n_adapters) my_id = -1;  // the next kernel reports it; no adapter is read for it
     // lanes that open an adapter: the first token of each distinct id
     const unsigned same = __match_any_sync(0xffffffffu, my_id);
     unsigned leaders = __ballot_sync(0xffffffffu, my_id >= 0 && (__ffs(same) - 1) == lane);
@@ -157,45 +142,80 @@ __device__ __forceinline__ float expand_dot(const __nv_bfloat16* __restrict__ b_
     return s;
 }
 
-// ------------------------------------------------------- streaming (m <= 64)
+// ------------------------------------------------------- streaming (m <= 32)
+// Every block takes an equal share of the output columns, 32 rows of W at a
+// time; its 16 warps split K, each through its own ring (stream_mma.cuh), and
+// add their sums in shared memory.  Only the adapters' part waits for the shrink
+// kernel, so W is on its way while that one runs.  Bound by reading W.
+constexpr int kStreamStages = 3;
+
 template <int NT>
 struct StreamSmem {
-    // double buffered where two fit into shared memory
-    static constexpr int kBufs = NT < 8 ? 2 : 1;
-    float red[kBufs][kWarps][2 * NT * 4][32];
+    unsigned char ring[kWarps][kStreamStages][kRingBytes];  // then the warps' sums
     float h[8 * NT][MOE_MAX_LORA_RANK + 1];
-    int id[8 * NT];
-    float scale[8 * NT];
+    int id[32], bad;
+    float scale[32];
 };
 
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) lora_stream_kernel(const LoraArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     StreamSmem<NT>& sm = *reinterpret_cast<StreamSmem<NT>*>(smem_raw);
+    static_assert(sizeof(sm.ring) >= sizeof(float) * kWarps * 2 * NT * 4 * 32, "sums lie in the ring");
+    float(*red)[2 * NT * 4][32] = reinterpret_cast<float(*)[2 * NT * 4][32]>(&sm.ring[0][0][0]);  // [kWarps]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c8 = (lane & 3) * 8;
-    if (*a.status != kDevOk) return;
-    const int m = static_cast<int>(a.m);
-    if (tid < m) {
-        const int id = a.adapter_ids[tid];
-        sm.id[tid] = id;
-        sm.scale[tid] = id >= 0 && a.scales ? a.scales[id] : 1.0f;
-    }
-    for (int u = tid; u < m * a.rank; u += kThreads) {
-        float s = a.h[u];
-        for (int z = 1; z < a.k_splits; ++z) s += a.h[static_cast<size_t>(z) * m * a.rank + u];
-        sm.h[u / a.rank][u % a.rank] = s;
-    }
+    const int g = lane >> 2;
+    const int m = static_cast<int>(a.m), nt = (m + 7) >> 3;
     const int lo = static_cast<int>(static_cast<long long>(a.n) * blockIdx.x / gridDim.x);
     const int hi = static_cast<int>(static_cast<long long>(a.n) * (blockIdx.x + 1) / gridDim.x);
-    const int nkb = (a.k + kKb - 1) / kKb;
-    const int nt = (m + 7) >> 3;
-    // steps go round robin over the warps; `rot` is the warp of a tile's first
-    // step, from which the partial sums are added (the order is K's alone)
-    int kb = warp, buf = 0, rot = 0;
+    const uint32_t ring = smem_u32(&sm.ring[warp][0][0]);
+    const __nv_bfloat16* tok[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) tok[n] = a.x + static_cast<size_t>(min(n * 8 + g, m - 1)) * a.k;
+
+    int fill_k = 0, fill_slot = 0, use_slot = 0;
     for (int n0 = lo; n0 < hi; n0 += kTileN) {
         const int nn = min(kTileN, hi - n0);
         const __nv_bfloat16* w = a.W + static_cast<size_t>(n0) * a.k;
+        const bool wide = nn <= 16;
+        const int step = wide ? 128 : 64;
+        const auto row = [&](int r) { return r < nn ? w + static_cast<size_t>(r) * a.k : nullptr; };
+        const auto fill = [&] {
+            if (fill_k < a.k) {
+                if (wide)
+                    ring_fill<true>(ring + fill_slot * kRingBytes, row, fill_k, a.k, lane);
+                else
+                    ring_fill<false>(ring + fill_slot * kRingBytes, row, fill_k, a.k, lane);
+            }
+            fill_k += kWarps * step;
+            cp_async_commit();
+            fill_slot = fill_slot + 1 == kStreamStages ? 0 : fill_slot + 1;
+        };
+        fill_k = warp * step;
+        fill_slot = use_slot = 0;
+        for (int i = 0; i < kStreamStages - 1; ++i) fill();
+        if (n0 == lo) {
+            // the ids, while the first weights are on their way: any outside
+            // [-1, n_adapters) and the call does nothing
+            if (warp == 0) {
+                const int id = lane < m ? a.adapter_ids[lane] : -1;
+                const bool bad = __any_sync(0xffffffffu, id < -1 || id >= a.n_adapters);
+                sm.id[lane] = id;
+                sm.scale[lane] = !bad && id >= 0 && a.scales ? a.scales[id] : 1.0f;
+                if (lane == 0) {
+                    sm.bad = bad;
+                    if (blockIdx.x == 0) *a.status = bad ? kDevBadId : kDevOk;
+                }
+            }
+            __syncthreads();
+            if (sm.bad) break;
+        }
+        // the adapters' rows of this tile, into the L2
+        for (int u = tid; u < m * kTileN; u += kThreads) {
+            const int r = u % kTileN, id = sm.id[u / kTileN];
+            if (r < nn && id >= 0)
+                prefetch_l2(a.B + (static_cast<size_t>(id) * a.n + n0 + r) * a.rank);
+        }
         float acc[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -203,60 +223,57 @@ __global__ void __launch_bounds__(kThreads, 1) lora_stream_kernel(const LoraArgs
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
-        for (; kb < nkb; kb += kWarps) {
-            uint4 wv[2][4];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int r = h * 8 + g;
-                    wv[s][h] = r < nn && k < a.k ? ld_stream_u4(w + static_cast<size_t>(r) * a.k + k) : zero_u4();
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int k = kb * kKb + s * 32 + c8;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n >= nt) break;
-                    const int t = min(n * 8 + g, m - 1);
-                    const uint4 xv = k < a.k
-                        ? *reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t) * a.k + k) : zero_u4();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) mma_pieces(acc[h][n], wv[s][2 * h], wv[s][2 * h + 1], xv);
-                }
+        for (int k0 = warp * step; k0 < a.k; k0 += kWarps * step) {
+            const uint32_t slot = ring + use_slot * kRingBytes;
+            const auto ready = [&] {
+                cp_async_wait_group<kStreamStages - 2>();
+                __syncwarp();
+                fill();
+            };
+            if (wide)
+                ring_multiply<true, NT, 1>(acc, slot, tok, nt, k0, a.k, lane, ready);
+            else
+                ring_multiply<false, NT, 1>(acc, slot, tok, nt, k0, a.k, lane, ready);
+            use_slot = use_slot + 1 == kStreamStages ? 0 : use_slot + 1;
+        }
+        if (n0 == lo) {
+            wait_for_previous_kernel();
+            for (int u = tid; u < m * a.rank; u += kThreads) {
+                float s = a.h[u];
+                for (int z = 1; z < a.k_splits; ++z) s += a.h[static_cast<size_t>(z) * m * a.rank + u];
+                sm.h[u / a.rank][u % a.rank] = s;
             }
         }
-        kb -= nkb;
+        cp_async_wait_group<0>();
+        __syncthreads();  // the ring is used up
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sm.red[buf][warp][(h * NT + n) * 4 + e][lane] = acc[h][n][e];
+                for (int e = 0; e < 4; ++e) red[warp][(h * NT + n) * 4 + e][lane] = acc[h][n][e];
         __syncthreads();
         // lane = output column of the tile, so that stores are contiguous
         for (int u = tid; u < m * kTileN; u += kThreads) {
-            const int row = u % kTileN, t = u / kTileN;
-            if (row >= nn) continue;
-            const int hne = ((row >> 4) * NT + (t >> 3)) * 4 + ((row >> 3) & 1) * 2 + (t & 1);
-            const int l = (row & 7) * 4 + ((t & 7) >> 1);
+            const int r = u % kTileN, t = u / kTileN;
+            if (r >= nn) continue;
+            const int hne = ((r >> 4) * NT + (t >> 3)) * 4 + ((r >> 3) & 1) * 2 + (t & 1);
+            const int l = (r & 7) * 4 + ((t & 7) >> 1);
             float v = 0.0f;
 #pragma unroll
-            for (int q = 0; q < kWarps; ++q) v += sm.red[buf][(q + rot) % kWarps][hne][l];
+            for (int q = 0; q < kWarps; ++q) v += red[q][hne][l];
             const int id = sm.id[t];
             if (id >= 0)
-                v += sm.scale[t] * expand_dot(a.B + (static_cast<size_t>(id) * a.n + n0 + row) * a.rank,
+                v += sm.scale[t] * expand_dot(a.B + (static_cast<size_t>(id) * a.n + n0 + r) * a.rank,
                                               sm.h[t], a.rank);
-            store_y(a.y, a.y_dtype, static_cast<size_t>(t) * a.n + n0 + row, v);
+            store_y(a.y, a.y_dtype, static_cast<size_t>(t) * a.n + n0 + r, v);
         }
-        rot = (rot + nkb) % kWarps;
-        if (StreamSmem<NT>::kBufs == 2)
-            buf ^= 1;
-        else
-            __syncthreads();
+        __syncthreads();
     }
+    // after a bad id: copies in flight, and this kernel must not end before the
+    // one whose memory the stream's next kernel may write
+    cp_async_wait_all();
+    wait_for_previous_kernel();
 }
 
 template <int NT>
@@ -267,8 +284,17 @@ cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
         return cudaFuncSetAttribute(lora_stream_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err != cudaSuccess) return err;
-    lora_stream_kernel<NT><<<num_sms, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.n < num_sms ? a.n : num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lora_stream_kernel<NT>, a);
 }
 
 }  // namespace
@@ -307,8 +333,7 @@ cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     if (a.m <= 8) return launch_stream<1>(a, num_sms, stream);
     if (a.m <= 16) return launch_stream<2>(a, num_sms, stream);
-    if (a.m <= 32) return launch_stream<4>(a, num_sms, stream);
-    return launch_stream<8>(a, num_sms, stream);
+    return launch_stream<4>(a, num_sms, stream);
 }
 
 }  // namespace moe

@@ -50,6 +50,10 @@ __device__ __forceinline__ void cp_async_16_l2(uint32_t dst_smem, const void* sr
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 constexpr int kRingBytes = 4096;  // one step of one warp
 
 // Byte offset of 16-byte piece j of ring row r.  Odd rows swap the 64-byte

@@ -21,9 +21,11 @@ SHAPES = [
     (9, 264, 4736, 40, 4),         # 32 columns per SM
     (20, 520, 5000, 16, 20),       # more than one tile per SM
     (32, 1024, 512, 64, 32),
-    (33, 136, 100, 16, 7),
-    (64, 256, 513, 32, 64),        # the largest streamed batch
-    (65, 256, 513, 32, 64),        # the smallest batch on tcgen05
+    (32, 256, 513, 32, 64),        # the largest streamed batch
+    (33, 136, 100, 16, 7),         # the smallest batch on tcgen05
+    (65, 256, 513, 32, 64),
+    (100, 4096, 512, 16, 10),      # K of one tile over a cluster of four CTA pairs
+    (260, 2048, 2300, 16, 5),      # over two
     (128, 64, 256, 8, 3),
     (201, 1000, 1501, 24, 40),
     (300, 2048, 130, 128, 2),
