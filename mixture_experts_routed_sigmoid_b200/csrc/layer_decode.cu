@@ -355,8 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
             s.pos = s.end;
             return;
         }
-        const int lo = tiles * b / blocks, hi = tiles * (b + 1) / blocks;
-        s.pos = lo + warp < hi ? s.round + lo + warp : s.end;
+        // Large batches: a round is four runs of tiles, and a block takes a part
+        // of each for four of its warps (one on each of the SM's schedulers), so
+        // that no block gets crowded experts alone.  (32 tokens on 8 experts: 258
+        // us instead of 271 with one run; on 245 experts 853 and 861.)  The warps
+        // of a block then share fewer token rows in the L1, which costs a single
+        // token 3%: it takes one run.
+        constexpr int kRuns = NT == 1 ? 1 : 4, kW = kWarps / kRuns;
+        const int run = warp / kW, first = tiles * run / kRuns, n = tiles * (run + 1) / kRuns - first;
+        const int lo = n * b / blocks, hi = n * (b + 1) / blocks;
+        s.pos = lo + warp % kW < hi ? s.round + first + lo + warp % kW : s.end;
     };
     // Tiles of at most `cap` rows whose rounds over the warps leave the least
     // of the last one idle.
