@@ -916,12 +916,12 @@ MOE_API moe_status_t moe_layer_decode(
 namespace {
 
 // K ranges of the adapters' first product on the streaming path: enough blocks
-// (up to 32 adapters of 32 tokens x 32 adapter rows x one range each) to
-// occupy the SMs, at least two steps of a block's 16 warps per range.  A
-// function of the shape alone.
+// (an adapter per token x 32 adapter rows x one range each) to occupy the SMs,
+// at least two steps of a block's 16 warps per range.  A function of the shape
+// alone.
 int lora_k_splits(long long m, int k, int rank) {
     if (m > moe::kLoraStreamMaxTokens) return 1;
-    const long long blocks = (m < 32 ? m : (m + 31) / 32 * 32) * ((rank + 31) / 32);
+    const long long blocks = m * ((rank + 31) / 32);
     const long long by_sms = blocks > 0 ? 148 / blocks : 1;
     const long long by_k = k / 2048;
     const long long s = by_sms < by_k ? by_sms : by_k;
@@ -1062,7 +1062,7 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.wait_limit_ns = moe::kDefaultWaitLimitNs;
     cudaError_t err;
     if (stream_w) {
-        err = moe::launch_lora_shrink(a, s);
+        err = moe::launch_lora_shrink(a, num_sms(), s);
         if (err != cudaSuccess) return cuda_fail(err, "adapter shrink launch");
         err = moe::launch_lora_stream(a, num_sms(), s);
     } else {

@@ -221,7 +221,7 @@ struct LoraArgs {
     int n, k, rank, r16, n_adapters, k_splits, y_dtype;
     unsigned long long wait_limit_ns;
 };
-cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream);
+cudaError_t launch_lora_shrink(const LoraArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream);
 // map_x: boxes of 128 rows; map_a: of `rank` rows of [n_adapters * rank, k].
 cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x, const CUtensorMap& map_a,

@@ -3,15 +3,22 @@
 //   y[t] = W x[t] + scales[a] * B[a] (A[a] x[t]),   a = adapter_ids[t]
 // (a = -1: the projection alone).
 //
-// Kernel 1 (shrink), m <= 32: h[t] = A[a] x[t].  An item is 32 consecutive tokens and
-//   one of the adapters that occur among them; only those tokens' rows of x
-//   are read.  The tokens are the rows of the MMA (stream_mma.cuh, with x in
-//   the place of the weights), the adapter's rank its columns; rows of other
-//   tokens are dropped by selection, never by a multiplication with zero, so
-//   an adapter that holds NaN or infinities reaches its own requests only.
-// Kernel 2, m <= 32: streams W once through mma.sync (stream_mma.cuh) and
-//   adds scales[a] * B[a] h in its epilogue.
+// m <= 32, here:
+// Kernel 1 (shrink): h[t] = A[a] x[t], one adapter of the call's at a time;
+//   only its own tokens' rows of x are read.  The tokens are the rows of the
+//   MMA (stream_mma.cuh, with x in the place of the weights), the adapter's
+//   rank its columns; rows of other tokens are dropped by selection, never by a
+//   multiplication with zero, so an adapter that holds NaN or infinities
+//   reaches its own requests only.
+// Kernel 2 streams W once through mma.sync (stream_mma.cuh) and adds scales[a]
+//   * B[a] h in its epilogue.  It starts beside kernel 1 and waits for it only
+//   before that epilogue.
+// Bound: reading W (4096 x 4096: 5.2 us at the copy rate) and the launches of
+// two kernels; 1 token of 8 adapters of rank 16 takes 15 us, 32 tokens of 64
+// adapters 21.5 us (graph replays).
 // Larger m: the two tcgen05 kernels of lora_gemm.cu.
+#include <algorithm>
+
 #include "launch.h"
 #include "stream_mma.cuh"
 
@@ -21,39 +28,31 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKb = 64;       // K columns of one warp step
-constexpr int kGroup = 32;    // tokens of a shrink item
 constexpr int kTileN = 32;    // output columns of a streaming tile
 
 // ------------------------------------------------------------------ shrink
-// grid: (token groups / groups per block, rank tiles x adapter lanes, K
-// ranges).  `ks` warps split the K of an item; a block holds 16 / ks token
-// groups.  Adapter lane j of L takes every L-th adapter of its tokens.  The
-// f32 sums of K range z go to h + z * m * rank; the reader adds the ranges in
-// order.
+// grid: (rank tiles x adapter lanes, K ranges).  A block's warps split its K
+// range of an adapter and add their sums in the order of K.  Adapter lane j of
+// L takes every L-th adapter of the tokens.  The f32 sums of K range z go to h
+// + z * m * rank; the reader adds the ranges in order.
 constexpr int kShrinkStages = 3;
 
-__device__ __forceinline__ void item_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-template <int NT>  // NT: groups of 8 rank rows per item
+template <int NT>  // NT: groups of 8 rank rows per block
 __global__ void __launch_bounds__(kThreads, 1)
-    lora_shrink_kernel(const LoraArgs a, int rank_tiles, int ks) {
+    lora_shrink_kernel(const LoraArgs a, int rank_tiles) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
     allow_next_kernel();  // it waits for this one's writes before it reads them
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2;
-    const int item = warp / ks, part = warp % ks;  // this warp's tokens and its share of K
-    const long long t0 = static_cast<long long>(blockIdx.x) * (kWarps / ks * kGroup) + item * kGroup;
-    int my_id = t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
+    int my_id = lane < a.m ? a.adapter_ids[lane] : -1;
     if (my_id >= a.n_adapters) my_id = -1;  // the next kernel reports it; no adapter is read for it
     // lanes that open an adapter: the first token of each distinct id
     const unsigned same = __match_any_sync(0xffffffffu, my_id);
     unsigned leaders = __ballot_sync(0xffffffffu, my_id >= 0 && (__ffs(same) - 1) == lane);
-    const int adapter_lanes = gridDim.y / rank_tiles, my_lane = blockIdx.y / rank_tiles;
-    const int r0 = static_cast<int>(blockIdx.y % rank_tiles) * NT * 8;
+    const int adapter_lanes = gridDim.x / rank_tiles, my_lane = blockIdx.x / rank_tiles;
+    const int r0 = static_cast<int>(blockIdx.x % rank_tiles) * NT * 8;
     const int nr = min(NT * 8, a.rank - r0), nt = (nr + 7) >> 3;
-    const int nkb = (a.k + kKb - 1) / kKb, shares = ks * gridDim.z, share = blockIdx.z * ks + part;
+    const int nkb = (a.k + kKb - 1) / kKb, shares = kWarps * gridDim.y, share = blockIdx.y * kWarps + warp;
     const int k_lo = static_cast<int>(static_cast<long long>(nkb) * share / shares) * kKb;
     const int k_hi = min(a.k, static_cast<int>(static_cast<long long>(nkb) * (share + 1) / shares) * kKb);
     unsigned char* ring_mem = smem_raw + warp * kShrinkStages * kRingBytes;
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
         const auto row = [&](int r) -> const __nv_bfloat16* {
-            return mine >> r & 1u ? a.x + (t0 + r) * a.k : nullptr;
+            return mine >> r & 1u ? a.x + static_cast<size_t>(r) * a.k : nullptr;
         };
         int fill_k = k_lo, fill_slot = 0, use_slot = 0;
         const auto fill = [&] {
@@ -96,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
             use_slot = use_slot + 1 == kShrinkStages ? 0 : use_slot + 1;
         }
-        // the item's warps add their partial sums, in the order of K; element
+        // the block's warps add their partial sums, in the order of K; element
         // (h, n, e): token h * 16 + (e / 2) * 8 + g, rank row n * 8 + 2 c + e % 2
         cp_async_wait_group<0>();
         __syncwarp();
@@ -107,17 +106,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) own[((h * NT + n) * 4 + e) * 32 + lane] = acc[h][n][e];
-        item_sync(1 + item, ks * 32);
-        const float* parts = reinterpret_cast<const float*>(smem_raw + item * ks * kShrinkStages * kRingBytes);
+        __syncthreads();
+        const float* parts = reinterpret_cast<const float*>(smem_raw);
         constexpr int kPart = kShrinkStages * kRingBytes / 4;
-        for (int u = part * 32 + lane; u < 2 * NT * 4 * 32; u += ks * 32) {
+        for (int u = tid; u < 2 * NT * 4 * 32; u += kThreads) {
             const int l = u & 31, hne = u >> 5, e = hne & 3, n = (hne >> 2) % NT, h = (hne >> 2) / NT;
             float v = 0.0f;
-            for (int w = 0; w < ks; ++w) v += parts[w * kPart + u];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += parts[w * kPart + u];
             const int token = h * 16 + (e >> 1) * 8 + (l >> 2), r = n * 8 + (l & 3) * 2 + (e & 1);
-            if ((mine >> token & 1u) && r < nr) a.h[(blockIdx.z * a.m + t0 + token) * a.rank + r0 + r] = v;
+            if ((mine >> token & 1u) && r < nr) a.h[(blockIdx.y * a.m + token) * a.rank + r0 + r] = v;
         }
-        item_sync(1 + item, ks * 32);
+        __syncthreads();
     }
 }
 
@@ -300,34 +300,25 @@ cudaError_t launch_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace
 
 template <int NT>
-static cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
+static cudaError_t launch_shrink(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     static PerDeviceOnce once;
     constexpr int smem = kWarps * kShrinkStages * kRingBytes;
     cudaError_t err = once.run([] {
         return cudaFuncSetAttribute(lora_shrink_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err != cudaSuccess) return err;
-    const long long groups = (a.m + kGroup - 1) / kGroup;
     const int rank_tiles = (a.rank + NT * 8 - 1) / (NT * 8);
-    // warps per item: as many (2 to 16) as keep all SMs' warps busy once
-    int ks = 16;
-    while (ks > 2 && groups * rank_tiles * ks > 148 * kWarps) ks /= 2;
-    const unsigned blocks = static_cast<unsigned>((groups * ks + kWarps - 1) / kWarps);
-    // a block per adapter for a few tokens, one for all of them when the
-    // token groups fill the SMs by themselves
-    const unsigned most = static_cast<unsigned>(a.m < kGroup ? a.m : kGroup);
-    unsigned lanes = 148 / (blocks * rank_tiles * a.k_splits);
-    lanes = lanes < 1 ? 1 : lanes > most ? most : lanes;
-    lora_shrink_kernel<NT><<<dim3(blocks, rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(
-        a, rank_tiles, ks);
+    // a block per adapter and K range while that fills the SMs once
+    const int fit = num_sms / (rank_tiles * a.k_splits), lanes = std::max(1, std::min(fit, static_cast<int>(a.m)));
+    lora_shrink_kernel<NT><<<dim3(rank_tiles * lanes, a.k_splits), kThreads, smem, stream>>>(a, rank_tiles);
     return cudaGetLastError();
 }
 
-cudaError_t launch_lora_shrink(const LoraArgs& a, cudaStream_t stream) {
-    if (a.rank <= 8) return launch_shrink<1>(a, stream);
-    if (a.rank <= 16) return launch_shrink<2>(a, stream);
-    if (a.rank <= 32) return launch_shrink<4>(a, stream);
-    return launch_shrink<8>(a, stream);
+cudaError_t launch_lora_shrink(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+    if (a.rank <= 8) return launch_shrink<1>(a, num_sms, stream);
+    if (a.rank <= 16) return launch_shrink<2>(a, num_sms, stream);
+    if (a.rank <= 32) return launch_shrink<4>(a, num_sms, stream);
+    return launch_shrink<8>(a, num_sms, stream);
 }
 
 cudaError_t launch_lora_stream(const LoraArgs& a, int num_sms, cudaStream_t stream) {

@@ -1,7 +1,8 @@
 // The projection with adapters for larger batches, in one tcgen05 GEMM:
 //   y[t] = W x[t] + B[a] (scales[a] h[t]),  a = adapter_ids[t],
 // with h = A x and its scaling from the shrink kernel, as two bf16 parts (hi,
-// lo: 16 significant bits).
+// lo: 16 significant bits, 2^-17 of the adapter's term; one part's 2^-9 would
+// show in an f32 y, and a third would cost half as much again).
 //
 // A CTA pair owns a tile of 256 tokens x `bn` output columns (M = 256, N = bn
 // MMAs over both CTAs; each CTA loads its 128 tokens and its half of W's rows,
@@ -11,9 +12,10 @@
 // which are zero for the tokens of other adapters.  So they cost 2 * rank / k of
 // the projection's MMAs per adapter of a tile, and no pass over y.
 //
-// Where tiles are few (SPLIT), a cluster of 1, 2 or 4 pairs takes one tile: each pair a part of K and of the adapters' stages.  The
-// partial tiles meet in distributed shared memory, and all warps of every CTA
-// add and store their share of the columns, pairs in order.
+// Where tiles are few (SPLIT), a cluster of 1, 2 or 4 pairs takes one tile: each
+// pair a part of K and of the adapters' stages.  The partial tiles meet in
+// distributed shared memory, and all warps of every CTA add and store their
+// share of the columns, pairs in order.
 //
 // The adapters' stages have two buffers of their own beside the ring, so they
 // are copied while the projection of the same tile runs (in the ring's order
@@ -28,8 +30,16 @@
 // epilogue, 8-11 copy the adapters' stages (cp.async: 16-byte pieces of h and B
 // picked by adapter).  A fence or a release waits for its thread's copies in
 // flight, so the threads that copy never fence (a stage took 3100 cycles when
-// they did).  Two accumulators let the epilogue of a tile overlap
-// the next tile's MMAs.  Every wait is bounded.
+// they did).  Two accumulators let the epilogue of a tile overlap the next
+// tile's MMAs.  Every wait is bounded.
+//
+// Bound by the tensor core: 4096 tokens of 4096 x 4096, 8 adapters of rank 16:
+// 116 us with the shrink kernel (1.18 PFLOP/s), 16384 tokens of 2048 x 4096, 16
+// adapters of rank 64, f32 out: 237 us (1.16).  The tensor core's accumulator
+// truncates, so over K = 2048 the sums are off by 2.4e-6 of y's size where f32
+// additions are off by 4e-7.
+#include <algorithm>
+
 #include "launch.h"
 #include "pair_mma.cuh"
 
@@ -886,9 +896,12 @@ cudaError_t launch_lora_shrink_gemm(const LoraArgs& a, const CUtensorMap& map_x,
     int split = 1;
     while (split < 8 && tiles * split * 2 <= 148 && (a.k + 63) / 64 >= split * 8) split *= 2;
     const long long rest = 148 / (tiles * split);
-    // adapters of a pass: up to 128 columns for small batches, whose tokens may
-    // all have adapters of their own; one for prompts (deeper ring)
-    const int group = tiles <= 16 ? 128 / a.r16 : 1;
+    // Adapters of a pass: up to 128 columns for small batches, whose tokens may
+    // all have adapters of their own, up to 64 for large ones, whose ring then
+    // is deeper.  (4096 x 4096, rank 16, 256 requests: 2048 tokens 172 us with one
+    // adapter a pass, 117 with eight; 8192 tokens 294, 258 with four, 270 with
+    // eight; with 4 requests 202, 205 and 209.)
+    const int group = std::max(1, (tiles <= 16 ? 128 : 64) / a.r16);
     const unsigned lanes = static_cast<unsigned>(rest < 2 ? 2 : rest > 128 ? 128 : rest);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), lanes);

@@ -160,8 +160,6 @@ __device__ __forceinline__ void ring_multiply(float (&acc)[2][NT][4], uint32_t s
     }
 }
 
-__device__ __forceinline__ uint4 zero_u4() { return make_uint4(0u, 0u, 0u, 0u); }
-
 // v as the sum of three bf16 values (24 significant bits): hi = bf16(v), mid =
 // bf16(v - hi), lo = bf16(v - hi - mid).  The MMA operands of an f32 value:
 // one bf16 keeps 8 bits and two keep 16, both short of the f32 product that
