@@ -138,10 +138,16 @@ __global__ void __launch_bounds__(kThreads) layer_router_kernel(
 }
 
 // ----------------------------------------------------------------- experts
-constexpr int kStages = 3;  // ring slots per warp: 2 steps in flight while one is used
+// Ring slots per warp: one holds the step that is used, the others are in
+// flight.  With several groups of 8 tokens the L1 that a third slot takes is
+// worth more for the token rows (13 tokens of 61 experts and a shared one: 148
+// us with two, 161 with three; 32 tokens on 16 experts 244 and 259), with one
+// the bytes in flight are (8 tokens of 53 experts: 360 and 348 us).
+__host__ __device__ constexpr int ring_slots(int nt) { return nt == 1 ? 3 : 2; }
 
+template <int SLOTS>
 struct ExpertsSmem {
-    unsigned char ring[kWarps][kStages][kRingBytes];  // first the routing keys, then weights
+    unsigned char ring[kWarps][SLOTS][kRingBytes];  // first the routing keys, then weights
     int key[kMaxRows], sorted[kMaxRows], perm[kMaxRows];
     int gexp[kMaxRows], gfirst[kMaxRows + 1];
     int slot_id[kMaxRows];
@@ -151,7 +157,7 @@ struct ExpertsSmem {
 // The block-combining variant keeps the down outputs of its 32 hidden rows in
 // shared memory, [routed rows, then shared rows][hidden row], behind ExpertsSmem;
 // this many rows fit.
-constexpr int kCombineRows = (232448 - static_cast<int>(sizeof(ExpertsSmem))) / ((kTileH + 1) * 4);
+constexpr int kCombineRows = (232448 - static_cast<int>(sizeof(ExpertsSmem<ring_slots(1)>))) / ((kTileH + 1) * 4);
 
 // Top-k of one token by (score + bias descending, expert ascending), by one
 // warp.  key: the warp's scratch of n_experts floats.  Each lane keeps the
@@ -244,7 +250,8 @@ struct Tile {
 // Expert map of the routed rows (rows <= kMaxRows): sm.perm lists them by
 // (expert, routed row); group q holds the rows of expert sm.gexp[q] at sorted
 // positions sm.gfirst[q] up to sm.gfirst[q + 1].  Returns the number of groups.
-__device__ __forceinline__ int map_rows(ExpertsSmem& sm, int rows) {
+template <class Smem>
+__device__ __forceinline__ int map_rows(Smem& sm, int rows) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     static_assert(MOE_MAX_EXPERTS * kMaxRows <= INT_MAX, "sort keys");
     const int mine = tid < rows ? sm.slot_id[tid] * kMaxRows + tid : INT_MAX;  // keys are distinct
@@ -286,8 +293,10 @@ __device__ __forceinline__ int map_rows(ExpertsSmem& sm, int rows) {
 template <int NT, bool COMBINE>
 __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerDecodeArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    ExpertsSmem& sm = *reinterpret_cast<ExpertsSmem*>(smem_raw);
-    float(*sm_d)[kTileH + 1] = reinterpret_cast<float(*)[kTileH + 1]>(smem_raw + sizeof(ExpertsSmem));
+    constexpr int kStages = ring_slots(NT);
+    using Smem = ExpertsSmem<kStages>;
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    float(*sm_d)[kTileH + 1] = reinterpret_cast<float(*)[kTileH + 1]>(smem_raw + sizeof(Smem));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int rows = a.m * a.top_k;
@@ -570,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
 template <int NT, bool COMBINE>
 cudaError_t launch_experts(const LayerDecodeArgs& args, int num_sms, cudaStream_t stream) {
     const int d_rows = COMBINE ? args.m * (args.top_k + (args.inter_sh > 0 ? 1 : 0)) : 0;
-    const int smem = static_cast<int>(sizeof(ExpertsSmem)) + d_rows * (kTileH + 1) * 4;
+    using Smem = ExpertsSmem<ring_slots(NT)>;
+    const int smem = static_cast<int>(sizeof(Smem)) + d_rows * (kTileH + 1) * 4;
     static PerDeviceOnce once;
     cudaError_t err = once.run([] {
         return cudaFuncSetAttribute(layer_experts_kernel<NT, COMBINE>,
