@@ -435,9 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
         for (int i = 0; i < kStages - 1; ++i) fill(down, h0);
     };
 
-    // 32 rows per tile read the tokens half as often; with four token groups
-    // the down phase's three parts leave no registers for it.
-    constexpr int kDownCap = NT == 4 ? 16 : kTileH;
+    // 32 rows per tile read the tokens half as often; with several token groups
+    // the down phase's three parts leave no registers for it (32 tokens of 126
+    // experts: 978 us with 32 rows, 857 with 16; 13 tokens 148 and 145).
+    constexpr int kDownCap = NT == 1 ? kTileH : 16;
     float acc[2][NT][4];
     const __nv_bfloat16* tok[NT];
     // Runs the warp's share after begin().
