@@ -370,8 +370,13 @@ MOE_API moe_status_t moe_layer_decode(
  * k and rank are multiples of 8, rank <= MOE_MAX_LORA_RANK (an adapter of
  * lower rank is padded with zero rows of A), 1 <= n <= 2^20, 1 <= n_adapters
  * <= MOE_MAX_ADAPTERS, m <= 2^24.  x, W, A, B and y are 16-byte aligned.
- * A row depends on its own token and adapter alone: NaN or infinities in
- * another adapter, or in another row of x, do not reach it.
+ * A row's value depends on its own token and adapter alone: NaN or infinities
+ * in another adapter, or in another row of x, do not reach it.  Its last bits
+ * can depend on m and on which adapters the other tokens have (they decide how
+ * K is split and how the adapters' part is added); the same call gives the
+ * same bits.  Above 32 tokens scales * A x is kept to 16 bits, |error| <= 2^-17
+ * of it, and the sums are the tensor core's f32 ones.  An adapter's product
+ * above bf16's largest value becomes infinite.
  * An id out of range sets MOE_ERR_DEVICE_BAD_ID in the ws status word
  * (moe_check_status) and leaves y unwritten.
  */

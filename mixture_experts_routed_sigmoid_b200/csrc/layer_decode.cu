@@ -29,7 +29,11 @@
 // nothing is rounded below f32.  A row's K order is the same wherever it
 // lands, so its bits depend on its own token alone.
 //
-// Measured (graph replays, 256 experts of 2048 x 768... unless said):
+// Measured (graph replays; 256 experts, hidden 4096, inter 1536, top-8): 1
+// token 70 us (4.3 TB/s over the call, 5.4 while it streams), 8 tokens of 53
+// experts 351 (5.7), 32 tokens of 126 experts 852 (5.6), 32 tokens on 16 experts
+// 243 (2.5: their token rows, through L1 and L2).  Before the first expert byte: 9 us
+// at 1 token, 24 at 32 (router 2.5 and 12, launch gap 2.6, routing 3.5 and 9).
 #include <climits>
 #include <math.h>
 
