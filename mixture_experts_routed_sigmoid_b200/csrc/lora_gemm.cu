@@ -26,18 +26,16 @@
 // and the epilogue adds the piece's products for the tokens that do use it.
 //
 // Warps per CTA: 0 copies the tiles (TMA), 1 issues the MMAs (leader CTA only),
-// 2 and 3 check the adapters' stages and announce them to the leader, 4-7
-// epilogue, 8-11 copy the adapters' stages (cp.async: 16-byte pieces of h and B
-// picked by adapter).  A fence or a release waits for its thread's copies in
+// 2 and 3 check the adapters' stages and announce them to the leader, 8-11 copy
+// those stages (cp.async: 16-byte pieces of h and B picked by adapter), 4-7 and
+// 12-15 are the epilogue.  A fence or a release waits for its thread's copies in
 // flight, so the threads that copy never fence (a stage took 3100 cycles when
-// they did).  Two accumulators let the epilogue of a tile overlap the next
-// tile's MMAs.  Every wait is bounded.
+// they did).  Two accumulators let the epilogue of one overlap the next one's
+// MMAs.  Every wait is bounded.
 //
-// Bound by the tensor core: 4096 tokens of 4096 x 4096, 8 adapters of rank 16:
-// 116 us with the shrink kernel (1.18 PFLOP/s), 16384 tokens of 2048 x 4096, 16
-// adapters of rank 64, f32 out: 237 us (1.16).  The tensor core's accumulator
-// truncates, so over K = 2048 the sums are off by 2.4e-6 of y's size where f32
-// additions are off by 4e-7.
+// Bound by the tensor core: 4096 tokens of 4096 x 4096, 8 adapters of rank 16,
+// bf16 out: 118 us with the shrink kernel (1.16 PFLOP/s); 16384 tokens of 2048 x
+// 4096, 16 adapters of rank 64, f32 out: 261 us (1.05).
 #include <algorithm>
 
 #include "launch.h"
@@ -49,12 +47,13 @@ namespace {
 constexpr int kMaxStages = 8;         // ring of the projection's stages
 constexpr int kExt = 2;               // stages of the adapters' columns, beside the ring
 constexpr int kHalf = 128 * 128;      // bytes of 128 rows x 64 columns
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kChunk = 8;             // stages of the projection per accumulator, at most (f32 output)
 constexpr int kTmemCols = 512;
 constexpr int kFixSlots = 4;
 constexpr int kPartPitch = 36;        // words of a partial tile's row of 32 columns
 constexpr int kPitch = 33;            // words of a staged epilogue row
-constexpr int kEpiBytes = 4 * 32 * kPitch * 4;
+constexpr int kEpiBytes = 8 * 16 * kPitch * 4;  // 16 rows of 32 columns per epilogue warp
 constexpr int kTail = kEpiBytes + 512 + kLoraTileRows * 4 + 1024;  // behind the stages, and alignment
 constexpr int kSmemLimit = 232448;
 // Bytes of a stage and the ring's stages for tiles of bn columns: 4 at 256, 5
@@ -90,8 +89,13 @@ __device__ __forceinline__ bool all_of_four_warps(bool v) {
     return r != 0;
 }
 
+// Barriers 2 to 5: the warps of one warpgroup (1 is the copying warps').
+__device__ __forceinline__ void warpgroup_sync(int warpgroup) {
+    asm volatile("bar.sync %0, 128;" ::"r"(2 + warpgroup) : "memory");
+}
+
 // Products of the pieces of B[adapter] row `col` that are not finite.
-__device__ __noinline__ float fix_up(const LoraArgs& a, long long t, int id, int col) {
+__device__ __forceinline__ float fix_up(const LoraArgs& a, long long t, int id, int col) {
     const __nv_bfloat16* b = a.B + (static_cast<size_t>(id) * a.n + col) * a.rank;
     const __nv_bfloat16* h = a.h_split + static_cast<size_t>(t) * 2 * a.r16;
     float s = 0.0f;
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const int stage_size = stage_bytes(bn), n_stages = ring_stages(bn);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (n_stages + kExt) * stage_size + kEpiBytes);  // leader's are used
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + (n_stages + kExt) * stage_size + kEpiBytes);  // leader's
     uint64_t* empty = full + kMaxStages;
     uint64_t* acc_full = empty + kMaxStages;   // [2]
     uint64_t* acc_empty = acc_full + 2;     // [2], leader's are used
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);  // the epilogue warps of both CTAs
+            mbar_init(&acc_empty[b], 16);  // the epilogue warps of both CTAs
         }
         for (int i = 0; i < kFixSlots; ++i) fix[i] = 0;
         *abort_flag = 0;
@@ -289,6 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nk_all = (a.k + 63) / 64, kb_lo = nk_all * part / parts;
     const int nk = nk_all * (part + 1) / parts - kb_lo;  // this pair's stages of the projection
     const int half = bn / 2;
+    // The tensor core's accumulator truncates: over K = 2048 its sums are off by
+    // 2.1e-6 of their size, over 16384 by 1.9e-5, where additions that round are off
+    // by 5e-7.  So an f32 output's sums are taken from it every 512 columns of K
+    // and added in registers (now 5e-7 at every K).  A bf16 output rounds by 2^-9
+    // and takes them once.  (16384 tokens of 2048 x 4096: 242 us without, 250 with
+    // 768 columns, 261 with 512: reading the accumulator slows the MMAs down.)
+    const int n_chunks = a.y_dtype == MOE_DTYPE_F32 ? (nk + kChunk - 1) / kChunk : 1;
+    const int chunk = (nk + n_chunks - 1) / n_chunks;
     // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
     // must have finished: waited for behind the first tile's projection, and
     // from the second tile on the count is loaded ahead of the tile.
@@ -314,248 +326,299 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stages once they are used up
     float* partial = reinterpret_cast<float*>(smem);
 
-    if (warp == 0) {
-        // ------------------------------------------------------ tile copies
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
+    // The epilogue's sums are 128 registers a thread: 4 warpgroups of 128 at
+    // launch become 80 + 176 + 80 + 176.
+    constexpr int kFewRegisters = 80, kManyRegisters = 176;
+    static_assert(2 * (kFewRegisters + kManyRegisters) <= 4 * 65536 / kThreads, "of those at launch");
+    if (((warp >> 2) & 1) == 0) {
+        registers_down<kFewRegisters>();
+        if (warp == 0) {
+            // ------------------------------------------------------ tile copies
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0;
+                bool good = true;
+                for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
+                    const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
+                    for (int kb = 0; kb < nk; ++kb) {
+                        if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
+                        const uint32_t bar = cluster_addr(smem_u32(&full[stage]), lead);
+                        uint8_t* sa = smem + stage * stage_size;
+                        // the leader expects both CTAs' bytes (an arrival from the other CTA
+                        // would need a release at cluster scope, 0.5 us a stage)
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
+                        tma_load_2d_pair(sa, &map_x, bar, (kb_lo + kb) * 64, mt * 256 + static_cast<int>(rank) * 128);
+                        tma_load_2d_pair(sa + kHalf, &map_w, bar, (kb_lo + kb) * 64,
+                                         nt * bn + static_cast<int>(rank) * half);
+                        advance(stage, phase);
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issuer
+            // The whole warp walks the loop and one elected lane issues: in a branch
+            // that only one lane enters, the compiler does not know the operands to
+            // be uniform, and the four MMAs of a stage took 489 cycles to issue.
+            if (rank == 0) {
+                int stage = 0, acc = 0, n = 0, seq = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                const bool leader = elect_one();
+                // instruction descriptor: M = 256, N = bn
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                                       (static_cast<uint32_t>(bn >> 3) << 17) | ((256u >> 4) << 24);
+                // the start address is the descriptor's low 14 bits (in 16 bytes); all
+                // of the ring lies below 2^18, so additions never carry out of it
+                const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+                bool good = true;
+                const auto finish_chunk = [&] {
+                    if (leader) umma_commit_pair(&acc_full[acc], lead);
+                    __syncwarp();
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1;
+                };
+                for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
+                    uint32_t d = 0;
+                    int first, steps = tile == cluster ? 0 : ext_steps(tile, first);
+                    bool ready = false;
+                    int in_chunk = chunk;  // stages that the accumulator has
+                    for (int kb = 0; kb < nk; ++kb, ++in_chunk) {
+                        if (in_chunk == chunk) {
+                            if (kb > 0) finish_chunk();
+                            in_chunk = 0;
+                            good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
+                            if (!good) break;
+                            tc_fence_after_sync();
+                            d = tmem + static_cast<uint32_t>(acc * 256);
+                        }
+                        good = __all_sync(0xffffffffu, ready || mbar_wait(&full[stage], phase, ctl));
+                        if (!good) break;
+                        tc_fence_after_sync();
+                        const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
+                        uint64_t* done = &empty[stage];
+                        advance(stage, phase);
+                        // the next stage's barrier is asked while these MMAs are issued
+                        if (kb + 1 < nk) ready = mbar_test(&full[stage], phase);
+                        if (leader) {
+#pragma unroll
+                            for (int k4 = 0; k4 < 4; ++k4)
+                                umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
+                                               (in_chunk | k4) != 0);
+                            umma_commit_pair(done, lead);
+                        }
+                        __syncwarp();
+                    }
+                    if (!good) break;
+                    if (tile == cluster) {
+                        wait_for_previous_kernel();
+                        steps = ext_steps(tile, first);
+                    }
+                    for (int left = steps; left > 0; left -= 4, ++n) {
+                        const int e = n % kExt;
+                        good = __all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl));
+                        if (!good) break;
+                        tc_fence_after_sync();
+                        const uint64_t da = desc0 + static_cast<uint64_t>((n_stages + e) * (stage_size >> 4));
+                        if (bad_ext[e] && lane == 0) {
+                            bad_ext[e] = 0;
+                            const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
+                            for (int q = 0; q < 2 * parts; ++q) st_shared_cluster(cluster_addr(at, q), tile + 1);
+                            fence_cluster();
+                        }
+                        __syncwarp();
+                        if (leader) {
+                            for (int k4 = 0; k4 < min(4, left); ++k4)
+                                umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
+                            umma_commit_pair(&ext_empty[e], lead);
+                        }
+                        __syncwarp();
+                    }
+                    if (!good) break;
+                    finish_chunk();
+                }
+            }
+            __syncwarp();
+        } else if (warp < 4) {
+            // ------------------------------------------------------ checking them
+            // a stage each
+            wait_for_previous_kernel();
+            const int e = warp - 2;
+            static_assert(kExt == 2, "one checking warp per stage");
+            uint8_t* sa = smem + (n_stages + e) * stage_size;
+            int n = 0;
             bool good = true;
             for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
-                const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!(good = mbar_wait_cluster(&empty[stage], phase ^ 1, ctl))) break;
-                    const uint32_t bar = cluster_addr(smem_u32(&full[stage]), lead);
-                    uint8_t* sa = smem + stage * stage_size;
-                    // the leader expects both CTAs' bytes (an arrival from the other CTA
-                    // would need a release at cluster scope, 0.5 us a stage)
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kHalf + half * 128));
-                    tma_load_2d_pair(sa, &map_x, bar, (kb_lo + kb) * 64, mt * 256 + static_cast<int>(rank) * 128);
-                    tma_load_2d_pair(sa + kHalf, &map_w, bar, (kb_lo + kb) * 64, nt * bn + static_cast<int>(rank) * half);
-                    advance(stage, phase);
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issuer
-        // The whole warp walks the loop and one elected lane issues: in a branch
-        // that only one lane enters, the compiler does not know the operands to
-        // be uniform, and the four MMAs of a stage took 489 cycles to issue.
-        if (rank == 0) {
-            int stage = 0, acc = 0, n = 0, seq = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            const bool leader = elect_one();
-            // instruction descriptor: M = 256, N = bn
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
-                                   (static_cast<uint32_t>(bn >> 3) << 17) | ((256u >> 4) << 24);
-            // the start address is the descriptor's low 14 bits (in 16 bytes); all
-            // of the ring lies below 2^18, so additions never carry out of it
-            const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-            bool good = true;
-            for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
-                good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
-                if (!good) break;
-                tc_fence_after_sync();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-                int first, steps = tile == cluster ? 0 : ext_steps(tile, first);
-                bool ready = false;
-                for (int kb = 0; kb < nk; ++kb) {
-                    good = __all_sync(0xffffffffu, ready || mbar_wait(&full[stage], phase, ctl));
-                    if (!good) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
-                    uint64_t* done = &empty[stage];
-                    advance(stage, phase);
-                    // the next stage's barrier is asked while these MMAs are issued
-                    if (kb + 1 < nk) ready = mbar_test(&full[stage], phase);
-                    if (leader) {
-#pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4)
-                            umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, (kb | k4) != 0);
-                        umma_commit_pair(done, lead);
-                    }
-                    __syncwarp();
-                }
-                if (!good) break;
-                if (tile == cluster) {
-                    wait_for_previous_kernel();
-                    steps = ext_steps(tile, first);
-                }
-                for (int left = steps; left > 0; left -= 4, ++n) {
-                    const int e = n % kExt;
-                    good = __all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl));
-                    if (!good) break;
-                    tc_fence_after_sync();
-                    const uint64_t da = desc0 + static_cast<uint64_t>((n_stages + e) * (stage_size >> 4));
-                    if (bad_ext[e] && lane == 0) {
-                        bad_ext[e] = 0;
-                        const uint32_t at = smem_u32(const_cast<int*>(&fix[seq % kFixSlots]));
-                        for (int q = 0; q < 2 * parts; ++q) st_shared_cluster(cluster_addr(at, q), tile + 1);
-                        fence_cluster();
-                    }
-                    __syncwarp();
-                    if (leader) {
-                        for (int k4 = 0; k4 < min(4, left); ++k4)
-                            umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, 1);
-                        umma_commit_pair(&ext_empty[e], lead);
-                    }
-                    __syncwarp();
-                }
-                if (!good) break;
-                if (leader) umma_commit_pair(&acc_full[acc], lead);
-                __syncwarp();
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1;
-            }
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ------------------------------------------------------ checking them
-        // a stage each
-        wait_for_previous_kernel();
-        const int e = warp - 2;
-        static_assert(kExt == 2, "one checking warp per stage");
-        uint8_t* sa = smem + (n_stages + e) * stage_size;
-        int n = 0;
-        bool good = true;
-        for (int tile = cluster; tile < n_tiles && good; tile += n_clusters) {
-            int first;
-            for (int left = ext_steps(tile, first); left > 0; left -= 4, ++n) {
-                if (n % kExt == e) {
-                    good = __all_sync(0xffffffffu, mbar_wait(&landed[e], n / kExt & 1u, ctl));
-                    if (!good) break;
-                    // pieces of B that are not finite become zeros (the epilogue
-                    // adds their products)
-                    uint4* b = reinterpret_cast<uint4*>(sa + kHalf) + lane;
-                    bool bad = false;
+                int first;
+                for (int left = ext_steps(tile, first); left > 0; left -= 4, ++n) {
+                    if (n % kExt == e) {
+                        good = __all_sync(0xffffffffu, mbar_wait(&landed[e], n / kExt & 1u, ctl));
+                        if (!good) break;
+                        // pieces of B that are not finite become zeros (the epilogue
+                        // adds their products)
+                        uint4* b = reinterpret_cast<uint4*>(sa + kHalf) + lane;
+                        bool bad = false;
 #pragma unroll 8
-                    for (int i = 0; i < half * 8 / 32; ++i) {
-                        if (not_finite_bf16x8(b[i * 32])) {
-                            b[i * 32] = make_uint4(0u, 0u, 0u, 0u);
-                            bad = true;
+                        for (int i = 0; i < half * 8 / 32; ++i) {
+                            if (not_finite_bf16x8(b[i * 32])) {
+                                b[i * 32] = make_uint4(0u, 0u, 0u, 0u);
+                                bad = true;
+                            }
+                        }
+                        if (bad) st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(&bad_ext[e])), lead), 1);
+                        fence_proxy_async_smem();  // the copies and the zeros, for the tensor core
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (rank == 0)
+                                mbar_arrive(&ext_full[e]);
+                            else
+                                mbar_arrive_cluster(cluster_addr(smem_u32(&ext_full[e]), lead));
                         }
                     }
-                    if (bad) st_shared_cluster(cluster_addr(smem_u32(const_cast<int*>(&bad_ext[e])), lead), 1);
-                    fence_proxy_async_smem();  // the copies and the zeros, for the tensor core
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0)
-                            mbar_arrive(&ext_full[e]);
-                        else
-                            mbar_arrive_cluster(cluster_addr(smem_u32(&ext_full[e]), lead));
+                }
+            }
+        } else {
+            // ------------------------------------------------------ adapters' stages
+            wait_for_previous_kernel();
+            // A thread copies piece tid % 8 of rows tid / 8 + 16 i: eight lanes take
+            // 128 contiguous bytes of a row (a row per lane would cost 32 memory
+            // transactions per instruction, 2000 cycles a stage).
+            const int pt = tid - 256, piece = pt & 7, row0 = pt >> 3;
+            const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row0 * 128 + ((piece ^ (row0 & 7)) << 4));
+            const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
+            int n = 0;
+            bool good = true;
+            for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
+                const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
+                const int count = max(a.tile_count[mt], 0);
+                // the warps go on or stop together; the last tile's list is read
+                if (!all_of_four_warps(good)) break;
+                for (int i = pt; i < count; i += 128)
+                    list[i] = a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + i];
+                all_of_four_warps(true);
+                const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + row0;
+                const int col0 = nt * bn + static_cast<int>(rank) * half + row0;
+                int id[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) id[i] = t0 + 16 * i < a.m ? a.adapter_ids[t0 + 16 * i] : -1;
+                // this thread's column among the adapters': adapter of the list and
+                // column within its 2 * r16
+                int first;
+                const int steps = ext_steps(tile, first);
+                int ad = (first * 16 + piece * 8) / (2 * a.r16), rem = first * 16 + piece * 8 - ad * 2 * a.r16;
+                for (int left = steps; left > 0; left -= 4, ++n) {
+                    const int e = n % kExt;
+                    if (!(good = mbar_wait_cluster(&ext_empty[e], (n / kExt & 1u) ^ 1u, ctl))) break;
+                    const uint32_t sa = ext + static_cast<uint32_t>((n_stages + e) * stage_size);
+                    const bool in = ad < count;
+                    const int adapter = in ? list[ad] : 0;
+                    const int r = rem < a.r16 ? rem : rem - a.r16;
+                    const bool b_in = in && r < a.rank;
+                    const __nv_bfloat16* h = a.h_split + t0 * 2 * a.r16 + rem;
+                    const __nv_bfloat16* b = a.B + adapter * b_adapter + static_cast<size_t>(col0) * a.rank + r;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool use = in && id[i] == adapter;
+                        cp_async_16(sa + i * 16 * 128, use ? h + i * 32 * a.r16 : a.h_split, use ? 16u : 0u);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (row0 + 16 * i >= half) break;
+                        const bool use = b_in && col0 + 16 * i < a.n;
+                        cp_async_16(sa + kHalf + i * 16 * 128, use ? b + i * 16 * a.rank : a.B, use ? 16u : 0u);
+                    }
+                    cp_async_arrive_noinc(&landed[e]);
+                    for (rem += 64; rem >= 2 * a.r16; rem -= 2 * a.r16) ++ad;
                 }
             }
+            cp_async_wait_all();
         }
-    } else if (warp >= 8) {
-        // ------------------------------------------------------ adapters' stages
-        wait_for_previous_kernel();
-        // A thread copies piece tid % 8 of rows tid / 8 + 16 i: eight lanes take
-        // 128 contiguous bytes of a row (a row per lane would cost 32 memory
-        // transactions per instruction, 2000 cycles a stage).
-        const int pt = tid - 256, piece = pt & 7, row0 = pt >> 3;
-        const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row0 * 128 + ((piece ^ (row0 & 7)) << 4));
-        const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
-        int n = 0;
-        bool good = true;
-        for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
-            const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
-            const int count = max(a.tile_count[mt], 0);
-            // the warps go on or stop together; the last tile's list is read
-            if (!all_of_four_warps(good)) break;
-            for (int i = pt; i < count; i += 128)
-                list[i] = a.tile_list[static_cast<size_t>(mt) * kLoraTileRows + i];
-            all_of_four_warps(true);
-            const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + row0;
-            const int col0 = nt * bn + static_cast<int>(rank) * half + row0;
-            int id[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) id[i] = t0 + 16 * i < a.m ? a.adapter_ids[t0 + 16 * i] : -1;
-            // this thread's column among the adapters': adapter of the list and
-            // column within its 2 * r16
-            int first;
-            const int steps = ext_steps(tile, first);
-            int ad = (first * 16 + piece * 8) / (2 * a.r16), rem = first * 16 + piece * 8 - ad * 2 * a.r16;
-            for (int left = steps; left > 0; left -= 4, ++n) {
-                const int e = n % kExt;
-                if (!(good = mbar_wait_cluster(&ext_empty[e], (n / kExt & 1u) ^ 1u, ctl))) break;
-                const uint32_t sa = ext + static_cast<uint32_t>((n_stages + e) * stage_size);
-                const bool in = ad < count;
-                const int adapter = in ? list[ad] : 0;
-                const int r = rem < a.r16 ? rem : rem - a.r16;
-                const bool b_in = in && r < a.rank;
-                const __nv_bfloat16* h = a.h_split + t0 * 2 * a.r16 + rem;
-                const __nv_bfloat16* b = a.B + adapter * b_adapter + static_cast<size_t>(col0) * a.rank + r;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const bool use = in && id[i] == adapter;
-                    cp_async_16(sa + i * 16 * 128, use ? h + i * 32 * a.r16 : a.h_split, use ? 16u : 0u);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (row0 + 16 * i >= half) break;
-                    const bool use = b_in && col0 + 16 * i < a.n;
-                    cp_async_16(sa + kHalf + i * 16 * 128, use ? b + i * 16 * a.rank : a.B, use ? 16u : 0u);
-                }
-                cp_async_arrive_noinc(&landed[e]);
-                for (rem += 64; rem >= 2 * a.r16; rem -= 2 * a.r16) ++ad;
-            }
+        __syncwarp();
+        if (SPLIT) {
+            warpgroup_sync(warp >> 2);  // between two register changes
+            registers_up<65536 / kThreads>();
         }
-        cp_async_wait_all();
-    } else if (warp >= 4) {
+    } else {
+        registers_up<kManyRegisters>();
         // ------------------------------------------------------ epilogue
+        // Two warps per 32 rows, each half of the tile's columns (32 at a time).
         wait_for_previous_kernel();
         const bool write = !any_bad_tile(a, n_tiles / n_col_tiles, lane);
         if (!write && blockIdx.x == 0 && tid == 128) set_status(a.status, kDevBadId);
-        const int quarter = warp & 3;
-        float* buf = epi + quarter * 32 * kPitch;
+        const int quarter = warp & 3, blocks = bn / 32;
+        const int c_lo = warp < 8 ? 0 : (blocks + 1) / 2, n_c = warp < 8 ? (blocks + 1) / 2 : blocks / 2;
+        float* buf = epi + (quarter + (warp < 8 ? 0 : 4)) * 16 * kPitch;
         int acc = 0, seq = 0;
         uint32_t acc_phase = 0;
         for (int tile = cluster; tile < n_tiles; tile += n_clusters, ++seq) {
             const int mt = tile / n_col_tiles, nt = tile - mt * n_col_tiles;
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], acc_phase, ctl))) break;
-            tc_fence_after_sync();
             const long long t0 = static_cast<long long>(mt) * 256 + rank * 128 + quarter * 32;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * 256);
-            if (SPLIT) {  // this pair's partial tile, for the whole cluster
-#pragma unroll 1
-                for (int c = 0; c < bn / 32; ++c) {
+            float sum[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[c][j] = 0.0f;
+            bool good = true;
+            for (int ch = 0; ch < n_chunks; ++ch) {
+                good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_full[acc], acc_phase, ctl));
+                if (!good) break;
+                tc_fence_after_sync();
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                       static_cast<uint32_t>(acc * 256 + c_lo * 32);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= n_c) break;  // warp-uniform
                     uint32_t v[32];
                     tmem_load_32cols(taddr + c * 32, v);
                     tmem_load_wait();
-                    float4* dst = reinterpret_cast<float4*>(partial + (c * 128 + quarter * 32 + lane) * kPartPitch);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(v[j]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[acc]), lead));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1;
+            }
+            if (!good) break;
+            if (SPLIT) {  // this pair's partial tile, for the whole cluster
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= n_c) break;
+                    float4* dst = reinterpret_cast<float4*>(
+                        partial + ((c_lo + c) * 128 + quarter * 32 + lane) * kPartPitch);
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        dst[j] = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                        dst[j] = make_float4(sum[c][4 * j], sum[c][4 * j + 1], sum[c][4 * j + 2], sum[c][4 * j + 3]);
                 }
                 break;
             }
-            const bool mend = write && fix[seq % kFixSlots] == tile + 1;
+            if (!write) continue;
+            const bool mend = fix[seq % kFixSlots] == tile + 1;
             const int id = mend && t0 + lane < a.m ? a.adapter_ids[t0 + lane] : -1;
-#pragma unroll 1
-            for (int c = 0; c < bn / 32; ++c) {
-                const int col0 = nt * bn + c * 32;
-                if (col0 >= a.n) break;
-                uint32_t v[32];
-                tmem_load_32cols(taddr + c * 32, v);
-                tmem_load_wait();
-                if (mend && id >= 0)
-                    for (int j = 0; j < 32; ++j)
-                        if (col0 + j < a.n)
-                            v[j] = __float_as_uint(__uint_as_float(v[j]) + fix_up(a, t0 + lane, id, col0 + j));
 #pragma unroll
-                for (int j = 0; j < 32; ++j) buf[lane * kPitch + j] = __uint_as_float(v[j]);
-                __syncwarp();
-                if (write) store_chunk<32>(a, buf, t0, col0, lane);
-                __syncwarp();
+            for (int c = 0; c < 4; ++c) {
+                const int col0 = nt * bn + (c_lo + c) * 32;
+                if (c >= n_c || col0 >= a.n) break;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {  // 16 rows at a time
+                    if (lane >> 4 == half) {
+                        float* row = buf + (lane & 15) * kPitch;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) row[j] = sum[c][j];
+                        if (id >= 0)
+                            for (int j = 0; j < 32; ++j)
+                                if (col0 + j < a.n) row[j] += fix_up(a, t0 + lane, id, col0 + j);
+                    }
+                    __syncwarp();
+                    store_chunk<16>(a, buf, t0 + half * 16, col0, lane);
+                    __syncwarp();
+                }
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[acc]), lead));
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1;
+        }
+        __syncwarp();
+        if (SPLIT) {
+            warpgroup_sync(warp >> 2);
+            registers_down<65536 / kThreads>();
         }
     }
     if (SPLIT) {
