@@ -370,6 +370,7 @@ MOE_API moe_status_t moe_layer_decode(
  * k and rank are multiples of 8, rank <= MOE_MAX_LORA_RANK (an adapter of
  * lower rank is padded with zero rows of A), 1 <= n <= 2^20, 1 <= n_adapters
  * <= MOE_MAX_ADAPTERS, m <= 2^24.  x, W, A, B and y are 16-byte aligned.
+ * y may not overlap x (MOE_ERR_INVALID_ARGUMENT) or any other input.
  * A row's value depends on its own token and adapter alone: NaN or infinities
  * in another adapter, or in another row of x, do not reach it.  Its last bits
  * can depend on m and on which adapters the other tokens have (they decide how

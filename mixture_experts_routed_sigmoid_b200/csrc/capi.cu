@@ -1031,6 +1031,11 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     MOE_TRY(check_ptr(y, "y", 16));
     const LoraLayout L = lora_layout(m, k, rank);
     MOE_TRY(check_ws(ws, ws_bytes, L.end));
+    // rows of y are written while rows of x are still read
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+    const size_t x_bytes = static_cast<size_t>(m) * k * 2;
+    const size_t y_bytes = static_cast<size_t>(m) * n * (y_dtype == MOE_DTYPE_BF16 ? 2 : 4);
+    if (x0 < y0 + y_bytes && y0 < x0 + x_bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "y overlaps x");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* wsb = static_cast<char*>(ws);
     const auto bf = [](const moe_bf16_t* p) { return reinterpret_cast<const __nv_bfloat16*>(p); };

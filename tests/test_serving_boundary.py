@@ -90,6 +90,16 @@ def test_matmul_lora_validation(lib, m):
     assert lib.moe_matmul_lora_workspace(0, 32, 64, 16, 4) > 0
 
 
+@pytest.mark.parametrize("dtype, elem", [(0, 4), (1, 2)])
+def test_matmul_lora_refuses_an_output_over_its_input(lib, dtype, elem):
+    x, rows, k, n = 1 << 20, 100, 64, 32
+    for y in (x, x + 16, x + rows * k * 2 - 16, x - rows * n * elem + 16):
+        assert _lora(lib, x=x, y=y, k=k, n=n, dtype=dtype) == INVALID
+        assert b"overlaps" in lib.moe_last_error()
+    for y in (x + rows * k * 2, x - rows * n * elem):  # side by side: only the workspace is refused
+        assert _lora(lib, x=x, y=y, k=k, n=n, dtype=dtype, ws_bytes=0) == WS_SMALL
+
+
 def test_python_boundary_refuses_before_the_library():
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError, match="CUDA"):
