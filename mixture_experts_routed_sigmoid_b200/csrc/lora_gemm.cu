@@ -327,8 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* partial = reinterpret_cast<float*>(smem);
 
     // The epilogue's sums are 128 registers a thread: 4 warpgroups of 128 at
-    // launch become 80 + 176 + 80 + 176.
-    constexpr int kFewRegisters = 80, kManyRegisters = 176;
+    // launch become 72 + 184 + 72 + 184.
+    constexpr int kFewRegisters = 72, kManyRegisters = 184;
     static_assert(2 * (kFewRegisters + kManyRegisters) <= 4 * 65536 / kThreads, "of those at launch");
     if (((warp >> 2) & 1) == 0) {
         registers_down<kFewRegisters>();
