@@ -424,9 +424,8 @@ def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor
     if bias is not None:
         _require_shape(bias, "bias", f32, dev, (n_experts,))
     inter_sh = 0
-    shared = (w_sh, W_sh_gate, W_sh_up, W_sh_down)
-    if any(t is not None for t in shared):
-        if any(t is None for t in shared):
+    if not (w_sh is W_sh_gate is W_sh_up is W_sh_down is None):
+        if w_sh is None or W_sh_gate is None or W_sh_up is None or W_sh_down is None:
             raise ValueError("a shared expert needs w_sh, W_sh_gate, W_sh_up and W_sh_down")
         inter_sh = W_sh_gate.shape[0]
         if inter_sh == 0:
@@ -436,19 +435,19 @@ def moe_layer_decode(x: torch.Tensor, W_router: torch.Tensor, bias: torch.Tensor
         _require_shape(W_sh_up, "W_sh_up", bf16, dev, (inter_sh, hidden))
         _require_shape(W_sh_down, "W_sh_down", bf16, dev, (hidden, inter_sh))
     if y is None:
-        y = torch.empty((m, hidden), dtype=f32, device=dev)
+        y = x.new_empty((m, hidden), dtype=f32)  # cheaper than torch.empty(..., device=dev)
     else:
         _require_shape(y, "y", f32, dev, (m, hidden))
     if ids is None:
-        ids = torch.empty((m, top_k), dtype=torch.int32, device=dev)
+        ids = x.new_empty((m, top_k), dtype=torch.int32)
     else:
         _require_shape(ids, "ids", torch.int32, dev, (m, top_k))
     if weights is None:
-        weights = torch.empty((m, top_k), dtype=f32, device=dev)
+        weights = x.new_empty((m, top_k), dtype=f32)
     else:
         _require_shape(weights, "weights", f32, dev, (m, top_k))
     if logits is None:
-        logits = torch.empty((m, n_experts), dtype=f32, device=dev)
+        logits = x.new_empty((m, n_experts), dtype=f32)
     else:
         _require_shape(logits, "logits", f32, dev, (m, n_experts))
     lib = load_library()
@@ -496,7 +495,7 @@ def moe_matmul_lora(x: torch.Tensor, W: torch.Tensor, adapter_ids: torch.Tensor,
     if out_dtype not in _Y_DTYPES:
         raise TypeError(f"the output must be torch.float32 or torch.bfloat16, got {out_dtype}")
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype, device=dev)
+        y = x.new_empty((m, n), dtype=out_dtype)
     else:
         _require_shape(y, "y", out_dtype, dev, (m, n))
     lib = load_library()
