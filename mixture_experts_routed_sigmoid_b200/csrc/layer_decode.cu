@@ -8,8 +8,8 @@
 // tests::exact_moe; hf2q qwen35/dense_ffn_arena.rs MoeFfnArena's shared
 // expert], the definitions of moe_router_topk and moe_ffn_forward_shared.
 //
-// Kernel 1 (router): a block computes the logits of two experts for all
-//   tokens, its 16 warps splitting K.  The sum is kept in f64 so that the
+// Kernel 1 (router): a block computes the logits of a few experts for a few
+//   tokens, its warps splitting K.  The sum is kept in f64 so that the
 //   choice of experts does not depend on the order of the additions: the
 //   rounded logits are those of the exact sum but for ties of the rounding.
 // Kernel 2 (experts): a cooperative grid of one block per SM.  Every block
@@ -33,7 +33,7 @@
 // token 70 us (4.3 TB/s over the call, 5.4 while it streams), 8 tokens of 53
 // experts 351 (5.7), 32 tokens of 126 experts 852 (5.6), 32 tokens on 16 experts
 // 243 (2.5: their token rows, through L1 and L2).  Before the first expert byte: 9 us
-// at 1 token, 24 at 32 (router 2.5 and 12, launch gap 2.6, routing 3.5 and 9).
+// at 1 token, 21 at 32 (router 2.5 and 9, launch gap 2.6, routing 3.5 and 9).
 #include <climits>
 #include <math.h>
 
@@ -49,7 +49,6 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileI = 16;   // intermediate rows of a gate/up tile (gate and up rows each)
 constexpr int kTileH = 32;   // hidden rows of a down tile
-constexpr int kMaxTokens = kLayerDecodeMaxTokens;
 constexpr int kMaxRows = kLayerDecodeMaxRows;
 
 __device__ __forceinline__ double sigmoid_f64(float v) {
@@ -57,81 +56,82 @@ __device__ __forceinline__ double sigmoid_f64(float v) {
 }
 
 // ------------------------------------------------------------------ router
-constexpr int kRouterRows = 2;    // experts per block
-constexpr int kRouterTokens = 4;  // tokens per pass over a warp's weights
-
-__global__ void __launch_bounds__(kThreads) layer_router_kernel(
+// A block takes ROWS experts (or the shared expert's gate) and TOK tokens; its
+// warps split K.  Converting to f64 costs four times a multiply-add, so each
+// converted weight serves TOK tokens and each converted x ROWS experts.  Few
+// tokens take 2 x 4 or 2 x 8, so that many blocks read the weights, more take 4
+// x 8, two blocks per SM.  (256 experts of 4096, against 2 x 4 with the tokens in
+// passes: 8 tokens 4.2 us and 5.0, 32 tokens 9.7 and 13.0; 64 experts of 1024, 32
+// tokens 4.0 and 8.2.)
+template <int ROWS, int TOK, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_router_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ W_router,
     const __nv_bfloat16* __restrict__ w_sh, int m, int hidden, int n_experts,
     float* __restrict__ logits, float* __restrict__ scores, float* __restrict__ gate,
     unsigned* __restrict__ barrier, int* __restrict__ status) {
-    __shared__ double part[kWarps][kRouterRows * kMaxTokens];
+    constexpr int kSums = ROWS * TOK, kLanes = 32 / kSums;  // lanes that end with the same sum
+    static_assert(kSums * kLanes == 32, "sums of a warp");
+    __shared__ double part[THREADS / 32][kSums];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         *barrier = 0;  // of the kernel that follows
         *status = kDevOk;
     }
     const int n_rows = n_experts + (w_sh ? 1 : 0);
-    const int r0 = blockIdx.x * kRouterRows;
-    const __nv_bfloat16* wrow[kRouterRows];
+    const int r0 = blockIdx.x * ROWS, t0 = blockIdx.y * TOK;
+    const __nv_bfloat16* wrow[ROWS];
 #pragma unroll
-    for (int j = 0; j < kRouterRows; ++j) {
+    for (int j = 0; j < ROWS; ++j) {
         const int r = min(r0 + j, n_rows - 1);
         wrow[j] = r < n_experts ? W_router + static_cast<size_t>(r) * hidden : w_sh;
     }
-    for (int t0 = 0; t0 < m; t0 += kRouterTokens) {
-        double acc[kRouterRows * kRouterTokens];
+    double acc[kSums];
 #pragma unroll
-        for (int i = 0; i < kRouterRows * kRouterTokens; ++i) acc[i] = 0.0;
-        for (int k = (warp * 32 + lane) * 8; k < hidden; k += kThreads * 8) {
-            float wf[kRouterRows][8];
+    for (int i = 0; i < kSums; ++i) acc[i] = 0.0;
+    for (int k = threadIdx.x * 8; k < hidden; k += THREADS * 8) {
+        float wf[ROWS][8];
 #pragma unroll
-            for (int j = 0; j < kRouterRows; ++j)
-                bf16x8_to_f32(*reinterpret_cast<const uint4*>(wrow[j] + k), wf[j]);
+        for (int j = 0; j < ROWS; ++j) bf16x8_to_f32(*reinterpret_cast<const uint4*>(wrow[j] + k), wf[j]);
+        uint4 xv[TOK];
 #pragma unroll
-            for (int q = 0; q < kRouterTokens; ++q) {
-                const int t = min(t0 + q, m - 1);
-                float xf[8];
-                bf16x8_to_f32(*reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * hidden + k), xf);
+        for (int q = 0; q < TOK; ++q)
+            xv[q] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(min(t0 + q, m - 1)) * hidden + k);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const double xd = xf[e];
+        for (int q = 0; q < TOK; ++q) {
+            float xf[8];
+            bf16x8_to_f32(xv[q], xf);
 #pragma unroll
-                    for (int j = 0; j < kRouterRows; ++j)
-                        acc[j * kRouterTokens + q] = fma(static_cast<double>(wf[j][e]), xd,
-                                                         acc[j * kRouterTokens + q]);
-                }
+            for (int e = 0; e < 8; ++e) {
+                const double xd = xf[e];
+#pragma unroll
+                for (int j = 0; j < ROWS; ++j)
+                    acc[j * TOK + q] = fma(static_cast<double>(wf[j][e]), xd, acc[j * TOK + q]);
             }
-        }
-        // 8 sums over 32 lanes: three steps that halve the sums a lane holds
-        // (it ends with sum number lane / 4), then two over the quad
-#pragma unroll
-        for (int h = 4; h >= 1; h >>= 1) {
-            const bool upper = lane & (h * 4);
-#pragma unroll
-            for (int i = 0; i < h; ++i) {
-                const double give = upper ? acc[i] : acc[i + h];
-                const double keep = upper ? acc[i + h] : acc[i];
-                acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, h * 4);
-            }
-        }
-        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 2);
-        acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], 1);
-        if ((lane & 3) == 0) {
-            const int i = lane >> 2;
-            const int t = t0 + i % kRouterTokens;
-            if (t < m) part[warp][(i / kRouterTokens) * kMaxTokens + t] = acc[0];
         }
     }
+    // the sums over 32 lanes: steps that halve the sums a lane holds (it ends
+    // with sum number lane / kLanes), then the rest
+#pragma unroll
+    for (int h = kSums / 2; h >= 1; h >>= 1) {
+        const bool upper = lane & (h * kLanes);
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const double give = upper ? acc[i] : acc[i + h];
+            const double keep = upper ? acc[i + h] : acc[i];
+            acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, h * kLanes);
+        }
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o >= 1; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+    if (lane % kLanes == 0) part[warp][lane / kLanes] = acc[0];
     __syncthreads();
-    const int j = threadIdx.x / kMaxTokens, t = threadIdx.x % kMaxTokens;
-    if (j < kRouterRows && r0 + j < n_rows && t < m) {
+    const int r = r0 + threadIdx.x / TOK, t = t0 + threadIdx.x % TOK;
+    if (threadIdx.x < kSums && r < n_rows && t < m) {
         double sum = 0.0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += part[w][j * kMaxTokens + t];
+        for (int w = 0; w < THREADS / 32; ++w) sum += part[w][threadIdx.x];
         const float l = static_cast<float>(sum);
         const float s = static_cast<float>(sigmoid_f64(l));
-        const int r = r0 + j;
         if (r < n_experts) {
             logits[static_cast<size_t>(t) * n_experts + r] = l;
             scores[static_cast<size_t>(t) * n_experts + r] = s;
@@ -611,9 +611,18 @@ cudaError_t launch_layer_decode(const LayerDecodeArgs& args, const __nv_bfloat16
                                 const __nv_bfloat16* w_sh, float* logits, int num_sms,
                                 cudaStream_t stream) {
     const int n_rows = args.n_experts + (args.inter_sh > 0 ? 1 : 0);
-    layer_router_kernel<<<(n_rows + kRouterRows - 1) / kRouterRows, kThreads, 0, stream>>>(
-        args.x, W_router, w_sh, args.m, args.hidden, args.n_experts, logits,
-        const_cast<float*>(args.scores), const_cast<float*>(args.gate), args.barrier, args.status);
+    float *scores = const_cast<float*>(args.scores), *gate = const_cast<float*>(args.gate);
+    const auto router = [&](auto kernel, int rows, int tokens, int threads) {
+        kernel<<<dim3((n_rows + rows - 1) / rows, (args.m + tokens - 1) / tokens), threads, 0, stream>>>(
+            args.x, W_router, w_sh, args.m, args.hidden, args.n_experts, logits, scores, gate, args.barrier,
+            args.status);
+    };
+    if (args.m <= 4)
+        router(layer_router_kernel<2, 4, 512>, 2, 4, 512);
+    else if (args.m <= 8)
+        router(layer_router_kernel<2, 8, 512>, 2, 8, 512);
+    else
+        router(layer_router_kernel<4, 8, 256>, 4, 8, 256);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     const int d_rows = args.m * (args.top_k + (args.inter_sh > 0 ? 1 : 0));
