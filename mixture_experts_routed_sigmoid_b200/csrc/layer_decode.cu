@@ -465,20 +465,32 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
                     for (int e = 0; e < 4; ++e) acc[h][n][e] = 0.0f;
             }
             const bool wide = t.n <= (kDown ? 16 : 8);
-            for (int k0 = 0; k0 < t.k; k0 += wide ? 128 : 64) {
-                const uint32_t slot = ring + use_slot * kRingBytes;
-                const auto ready = [&] {
-                    cp_async_wait_group<kStages - 2>();
-                    __syncwarp();
-                    // every lane has read the slot of the step before: it is free
-                    fill(kDown, h0);
-                };
-                if (wide || (kDown && kDownCap == 16))
-                    ring_multiply<true, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
-                else
-                    ring_multiply<false, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
-                use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
-            }
+            const auto ready = [&] {
+                cp_async_wait_group<kStages - 2>();
+                __syncwarp();
+                // every lane has read the slot of the step before: it is free
+                fill(kDown, h0);
+            };
+            const auto steps = [&](auto wide_tag) {
+                constexpr bool kWide = decltype(wide_tag)::value;
+                constexpr int kStep = kWide ? 128 : 64;
+                TokenPieces<kParts> ahead[2];
+                if (NT == 1) first_tokens<kWide>(ahead, tok[0], 0, t.k, kStep, lane);
+                for (int k0 = 0; k0 < t.k; k0 += kStep) {
+                    const uint32_t slot = ring + use_slot * kRingBytes;
+                    if constexpr (NT == 1) {
+                        ready();
+                        ring_multiply_one<kWide>(acc, slot, ahead, tok[0], k0, t.k, kStep, lane);
+                    } else {
+                        ring_multiply<kWide, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
+                    }
+                    use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
+                }
+            };
+            if (wide || (kDown && kDownCap == 16))
+                steps(std::true_type{});
+            else
+                steps(std::false_type{});
             finish(t, nt);
         }
     };

@@ -160,6 +160,43 @@ __device__ __forceinline__ void ring_multiply(float (&acc)[2][NT][4], uint32_t s
     }
 }
 
+// The same for one group of tokens, whose operands are loaded a step ahead:
+// t holds those of this step's two halves (WIDE), or of this step and the next.
+// `stride` columns lie between the warp's steps.
+template <bool WIDE, int PARTS>
+__device__ __forceinline__ void first_tokens(TokenPieces<PARTS> (&t)[2], const __nv_bfloat16* tok, int k0, int k,
+                                             int stride, int lane) {
+    t[0].load(tok, k0, k, lane);
+    t[1].load(tok, k0 + (WIDE ? 64 : stride), k, lane);
+}
+template <bool WIDE, int PARTS>
+__device__ __forceinline__ void ring_multiply_one(float (&acc)[2][1][4], uint32_t slot, TokenPieces<PARTS> (&t)[2],
+                                                  const __nv_bfloat16* tok, int k0, int k, int stride, int lane) {
+    constexpr int kHalves = WIDE ? 2 : 1, kTiles = WIDE ? 1 : 2;
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int half = 0; half < kHalves; ++half) {
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const uint4 lo = ld_shared_u4(slot + ring_offset<WIDE>(h * 16 + g, half * 8 + s * 4 + c));
+                const uint4 hi = ld_shared_u4(slot + ring_offset<WIDE>(h * 16 + 8 + g, half * 8 + s * 4 + c));
+#pragma unroll
+                for (int z = PARTS - 1; z >= 0; --z) mma_pieces(d, lo, hi, t[half].v[s][z]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[h][0][e] += d[e];
+        }
+        if (WIDE) t[half].load(tok, k0 + stride + half * 64, k, lane);
+    }
+    if (!WIDE) {
+        t[0] = t[1];
+        t[1].load(tok, k0 + 2 * stride, k, lane);
+    }
+}
+
 // v as the sum of three bf16 values (24 significant bits): hi = bf16(v), mid =
 // bf16(v - hi), lo = bf16(v - hi - mid).  The MMA operands of an f32 value:
 // one bf16 keeps 8 bits and two keep 16, both short of the f32 product that
