@@ -377,7 +377,7 @@ MOE_API moe_status_t moe_layer_decode(
  * K is split and how the adapters' part is added); the same call gives the
  * same bits.  Above 32 tokens scales * A x is kept to 16 bits, |error| <= 2^-17
  * of it (a value above bf16's largest becomes infinite); the projection's sums
- * are f32 ones, taken from the tensor core every 512 columns of k where y is f32.
+ * are f32 ones, taken from the tensor core every 768 columns of k where y is f32.
  * An id out of range sets MOE_ERR_DEVICE_BAD_ID in the ws status word
  * (moe_check_status) and leaves y unwritten.
  */

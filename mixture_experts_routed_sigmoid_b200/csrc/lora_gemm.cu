@@ -48,7 +48,7 @@ constexpr int kMaxStages = 8;         // ring of the projection's stages
 constexpr int kExt = 2;               // stages of the adapters' columns, beside the ring
 constexpr int kHalf = 128 * 128;      // bytes of 128 rows x 64 columns
 constexpr int kThreads = 512;
-constexpr int kChunk = 8;             // stages of the projection per accumulator, at most (f32 output)
+constexpr int kChunk = 12;            // stages of the projection per accumulator, at most (f32 output)
 constexpr int kTmemCols = 512;
 constexpr int kFixSlots = 4;
 constexpr int kPartPitch = 36;        // words of a partial tile's row of 32 columns
@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = bn / 2;
     // The tensor core's accumulator truncates: over K = 2048 its sums are off by
     // 2.1e-6 of their size, over 16384 by 1.9e-5, where additions that round are off
-    // by 5e-7.  So an f32 output's sums are taken from it every 512 columns of K
-    // and added in registers (now 5e-7 at every K).  A bf16 output rounds by 2^-9
-    // and takes them once.  (16384 tokens of 2048 x 4096: 242 us without, 250 with
-    // 768 columns, 261 with 512: reading the accumulator slows the MMAs down.)
-    const int n_chunks = a.y_dtype == MOE_DTYPE_F32 ? (nk + kChunk - 1) / kChunk : 1;
-    const int chunk = (nk + n_chunks - 1) / n_chunks;
+    // by 5e-7.  So an f32 output's sums are taken from it every 768 columns of K
+    // and added in registers (6.5e-7 at every K).  A bf16 output rounds by 2^-9
+    // and takes them once.  (16384 tokens of 2048 x 4096: 242 us without, 250
+    // with 768 columns, 261 with 512: the two accumulators then hold too little
+    // work to cover the stores of a tile.)
+    const int chunk = a.y_dtype == MOE_DTYPE_F32 ? kChunk : nk, n_chunks = (nk + chunk - 1) / chunk;
     // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
     // must have finished: waited for behind the first tile's projection, and
     // from the second tile on the count is loaded ahead of the tile.
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
         prefetch_tensormap(&map_a);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, MOE_MAX_LORA_RANK);
+        tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -810,6 +810,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 
     const int nkb = (a.k + 63) / 64;
     const int kb_lo = nkb * rank / split, kb_hi = nkb * (rank + 1) / split;
+    // for an f32 output up to four accumulators of 8 stages (more where K is
+    // longer) each, against the tensor core's truncation (see the projection)
+    const int n_kb = kb_hi - kb_lo, n_sums = a.y_dtype == MOE_DTYPE_F32 ? min((n_kb + 7) / 8, 4) : 1;
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0;
     const auto advance = [&] {
@@ -843,10 +846,13 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                 if (!good) break;
                 tc_fence_after_sync();
                 const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
+                const int q = (kb - kb_lo) * n_sums / n_kb;
+                const bool more = kb > kb_lo && (kb - 1 - kb_lo) * n_sums / n_kb == q;
                 if (leader) {
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4)
-                        umma_bf16(tmem, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc, kb > kb_lo || k4 > 0);
+                        umma_bf16(tmem + q * MOE_MAX_LORA_RANK, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
+                                  more || k4 > 0);
                     umma_commit(&empty[stage]);
                 }
                 __syncwarp();
@@ -859,13 +865,20 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             tc_fence_after_sync();
             if (good)
                 for (int c = 0; c < (here * a.r16 + 31) / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_load_32cols(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c * 32, v);
-                    tmem_load_wait();
+                    float sum[32];
+                    for (int q = 0; q < n_sums; ++q) {
+                        uint32_t v[32];
+                        tmem_load_32cols(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                                             q * MOE_MAX_LORA_RANK + c * 32, v);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sum[i] = q == 0 ? __uint_as_float(v[i]) : sum[i] + __uint_as_float(v[i]);
+                    }
                     float* row = sums + ((warp & 3) * 32 + lane) * pitch + c * 32;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c * 32 + i < cols) row[i] = __uint_as_float(v[i]);
+                        if (c * 32 + i < cols) row[i] = sum[i];
                 }
             tc_fence_before_sync();
             acc_phase ^= 1;
@@ -938,7 +951,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, MOE_MAX_LORA_RANK);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 

@@ -192,8 +192,8 @@ def test_two_streams_with_workspaces_of_their_own():
 @pytest.mark.parametrize("m, n", [(300, 512), (2100, 4096)])
 def test_long_sums_in_f32(m, n):
     """An f32 output does not lose more with a longer K: the tensor core truncates its sums, so they
-    are taken from it every 512 columns.  32 instructions of at most 2^-23 each to a partial sum,
-    whose errors are independent of the next ones', then k / 512 roundings of 2^-24."""
+    are taken from it every 768 columns.  48 instructions of at most 2^-23 each to a partial sum,
+    whose errors are independent of the next ones', then k / 768 roundings of 2^-24."""
     k = 16384
     g = torch.Generator(device="cuda").manual_seed(5)
     x, W = (torch.randn(r, k, device="cuda", generator=g).bfloat16() for r in (m, n))
@@ -202,7 +202,7 @@ def test_long_sums_in_f32(m, n):
     y = moe.moe_matmul_lora(x, W, ids, A, B, None, out_dtype=torch.float32).double()
     want = x.double() @ W.double().T
     off = ((y - want).norm() / want.norm()).item()
-    assert off <= (32 * 2 + k // 512) * ref.U
+    assert off <= (48 * 2 + k // 768) * ref.U
 
 
 def test_empty_batch():
