@@ -935,7 +935,8 @@ int lora_k_splits(long long m, int k, int rank) {
 // parts of a split one about 3000 + 10 per column.  A split tile is one
 // cluster of 4 or 8 CTAs, of which 33 or 15 fit on the GPU at once (the
 // occupancy query's answer).
-// (Measured at 4096 x 4096 x 4096: 192 columns 92 us, 256 columns 99.)
+// (Measured with the first product: 4096 tokens of 4096 x 4096, 192 columns 119
+// us, 224 136, 256 123; 16384 of 2048 x 4096, 192 columns 268 us, 256 249.)
 struct LoraTile {
     int columns, split;
 };

@@ -30,9 +30,9 @@
 // lands, so its bits depend on its own token alone.
 //
 // Measured (graph replays; 256 experts, hidden 4096, inter 1536, top-8): 1
-// token 70 us (4.3 TB/s over the call, 5.4 while it streams), 8 tokens of 53
-// experts 351 (5.7), 32 tokens of 126 experts 852 (5.6), 32 tokens on 16 experts
-// 243 (2.5: their token rows, through L1 and L2).  Before the first expert byte: 9 us
+// token 67 us (4.5 TB/s over the call, 5.6 while it streams), 8 tokens of 53
+// experts 349 (5.7), 32 tokens of 126 experts 850 (5.6), 32 tokens on 16 experts
+// 239 (2.5: their token rows, through L1 and L2).  Before the first expert byte: 9 us
 // at 1 token, 21 at 32 (router 2.5 and 9, launch gap 2.6, routing 3.5 and 9).
 #include <climits>
 #include <math.h>

@@ -5,8 +5,8 @@
 // whole K on its own, so no partial sums cross warps and no block-wide barrier
 // stands in the stream.  Its weights arrive through a ring in shared memory
 // that only this warp fills and reads (cp.async, 16 bytes per lane and copy):
-// 4 KB per step, as 32 rows x 64 columns or 16 rows x 128.  The ring keeps
-// 8 KB or more per warp in flight without holding registers, across tile ends
+// 4 KB per step, as 32 rows x 64 columns or 16 rows x 128.  The ring keeps 4 or
+// 8 KB per warp in flight without holding registers, across tile ends
 // and grid barriers.
 //
 // Which K columns an instruction's k index means is free as long as both
