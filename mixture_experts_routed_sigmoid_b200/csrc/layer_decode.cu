@@ -474,17 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
             const auto steps = [&](auto wide_tag) {
                 constexpr bool kWide = decltype(wide_tag)::value;
                 constexpr int kStep = kWide ? 128 : 64;
-                TokenPieces<kParts> ahead[2];
-                if (NT == 1) first_tokens<kWide>(ahead, tok[0], 0, t.k, kStep, lane);
-                for (int k0 = 0; k0 < t.k; k0 += kStep) {
-                    const uint32_t slot = ring + use_slot * kRingBytes;
-                    if constexpr (NT == 1) {
+                if (NT == 1 || nt == 1) {
+                    TokenPieces<kParts> ahead[2];
+                    first_tokens<kWide>(ahead, tok[0], 0, t.k, kStep, lane);
+                    for (int k0 = 0; k0 < t.k; k0 += kStep) {
                         ready();
-                        ring_multiply_one<kWide>(acc, slot, ahead, tok[0], k0, t.k, kStep, lane);
-                    } else {
-                        ring_multiply<kWide, NT, kParts>(acc, slot, tok, nt, k0, t.k, lane, ready);
+                        ring_multiply_one<kWide>(acc, ring + use_slot * kRingBytes, ahead, tok[0], k0, t.k, kStep, lane);
+                        use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
                     }
-                    use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
+                } else {
+                    for (int k0 = 0; k0 < t.k; k0 += kStep) {
+                        ring_multiply<kWide, NT, kParts>(acc, ring + use_slot * kRingBytes, tok, nt, k0, t.k, lane, ready);
+                        use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
+                    }
                 }
             };
             if (wide || (kDown && kDownCap == 16))

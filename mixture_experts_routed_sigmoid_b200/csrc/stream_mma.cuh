@@ -169,8 +169,8 @@ __device__ __forceinline__ void first_tokens(TokenPieces<PARTS> (&t)[2], const _
     t[0].load(tok, k0, k, lane);
     t[1].load(tok, k0 + (WIDE ? 64 : stride), k, lane);
 }
-template <bool WIDE, int PARTS>
-__device__ __forceinline__ void ring_multiply_one(float (&acc)[2][1][4], uint32_t slot, TokenPieces<PARTS> (&t)[2],
+template <bool WIDE, int PARTS, int NT>
+__device__ __forceinline__ void ring_multiply_one(float (&acc)[2][NT][4], uint32_t slot, TokenPieces<PARTS> (&t)[2],
                                                   const __nv_bfloat16* tok, int k0, int k, int stride, int lane) {
     constexpr int kHalves = WIDE ? 2 : 1, kTiles = WIDE ? 1 : 2;
     const int g = lane >> 2, c = lane & 3;
