@@ -332,6 +332,8 @@ MOE_API moe_status_t moe_ffn_forward_shared(
  * MOE_LAYER_DECODE_MAX_ROWS (else MOE_ERR_UNSUPPORTED_SHAPE: larger batches
  * take moe_router_topk and moe_ffn_forward_shared); hidden, inter and inter_sh
  * are multiples of 8.
+ * Batches that crowd more than about 8 tokens on every chosen expert are faster
+ * there too (grouped GEMMs, with an fp16 activation).
  * The logits are sums in f64, rounded once to f32, so which experts are
  * chosen does not depend on the order of the additions; moe_router_topk adds
  * in f32, and its choice can differ where two keys are that close.  The
