@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_router_
 // ----------------------------------------------------------------- experts
 // Ring slots per warp: one holds the step that is used, the others are in
 // flight.  With several groups of 8 tokens the L1 that a third slot takes is
-// worth more for the token rows (13 tokens of 61 experts and a shared one: 148
-// us with two, 161 with three; 32 tokens on 16 experts 244 and 259), with one
-// the bytes in flight are (8 tokens of 53 experts: 360 and 348 us).
+// worth more for the token rows (32 tokens of 126 experts: 768 us with two, 790
+// with three; on 16 experts 237 and 246), with one the bytes in flight are (8
+// tokens of 53 experts: 360 and 348 us).
 __host__ __device__ constexpr int ring_slots(int nt) { return nt == 1 ? 3 : 2; }
 
 template <int SLOTS>
@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
         }
         // Large batches: a round is four runs of tiles, and a block takes a part
         // of each for four of its warps (one on each of the SM's schedulers), so
-        // that no block gets crowded experts alone.  (32 tokens on 8 experts: 258
-        // us instead of 271 with one run; on 245 experts 853 and 861.)  The warps
+        // that no block gets crowded experts alone.  (32 tokens on 16 experts: 258
+        // us instead of 271 with one run; on 126 experts 853 and 861.)  The warps
         // of a block then share fewer token rows in the L1, which costs a single
         // token 3%: it takes one run.
         constexpr int kRuns = NT == 1 ? 1 : 4, kW = kWarps / kRuns;
@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
 
     // 32 rows per tile read the tokens half as often; with several token groups
     // the down phase's three parts leave no registers for it (32 tokens of 126
-    // experts: 978 us with 32 rows, 857 with 16; 13 tokens 148 and 145).
+    // experts: 795 us with 32 rows, 768 with 16; 13 tokens 140 and 131; only on
+    // 16 experts 227 and 237).
     constexpr int kDownCap = NT == 1 ? kTileH : 16;
     float acc[2][NT][4];
     const __nv_bfloat16* tok[NT];
@@ -479,12 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1) layer_experts_kernel(const LayerD
                     first_tokens<kWide>(ahead, tok[0], 0, t.k, kStep, lane);
                     for (int k0 = 0; k0 < t.k; k0 += kStep) {
                         ready();
-                        ring_multiply_one<kWide>(acc, ring + use_slot * kRingBytes, ahead, tok[0], k0, t.k, kStep, lane);
+                        ring_multiply_one<kWide>(acc, ring + use_slot * kRingBytes, ahead, tok[0], k0, t.k, kStep,
+                                                 lane);
                         use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
                     }
                 } else {
                     for (int k0 = 0; k0 < t.k; k0 += kStep) {
-                        ring_multiply<kWide, NT, kParts>(acc, ring + use_slot * kRingBytes, tok, nt, k0, t.k, lane, ready);
+                        ring_multiply<kWide, NT, kParts>(acc, ring + use_slot * kRingBytes, tok, nt, k0, t.k, lane,
+                                                         ready);
                         use_slot = use_slot + 1 == kStages ? 0 : use_slot + 1;
                     }
                 }

@@ -84,6 +84,26 @@ def test_without_bias_and_with_crowded_experts():
     check(c, got)
 
 
+@pytest.mark.parametrize("m, crowd", [(10, 1), (16, 2), (24, 1), (25, 2), (32, 1), (32, 3)])
+def test_crowded_experts_at_ragged_sizes(m, crowd):
+    """All tokens on `crowd` experts (2 to 4 groups of 8 tokens each) and one of the others' choice."""
+    c = make(m, 328, 200, 20, crowd + 1, 24, seed=40 + m + crowd)
+    c["bias"][:crowd] = 2.0
+    got = call(c)
+    for e in range(crowd):
+        assert ((got[1] == e).sum(1) == 1).all()
+    check(c, got)
+
+
+def test_a_row_has_the_same_bits_alone_and_in_a_crowd():
+    c = make(32, 328, 200, 12, 3, 24, seed=50)
+    whole = call(c)
+    for m in (1, 5, 8, 9, 16, 17, 25):
+        part = call(dict(c, x=c["x"][:m].contiguous()))
+        for a, b in zip(whole, part):
+            assert torch.equal(a[:m].view(torch.int32), b.view(torch.int32))
+
+
 def test_equal_keys_take_the_lower_expert():
     c = make(6, 128, 64, 48, 5, 0, seed=4, with_bias=False)
     c["W_router"][:] = c["W_router"][0]       # all logits of a token are equal
