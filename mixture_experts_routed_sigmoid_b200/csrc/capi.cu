@@ -916,7 +916,7 @@ MOE_API moe_status_t moe_layer_decode(
 namespace {
 
 // K ranges of the adapters' first product on the streaming path: enough blocks
-// (an adapter per token x 32 adapter rows x one range each) to occupy the SMs,
+// (an adapter per token, 32 rank rows on two SMs, one range each) for the SMs,
 // at least two steps of a block's 16 warps per range.  A function of the shape
 // alone.
 int lora_k_splits(long long m, int k, int rank) {

@@ -201,7 +201,8 @@ cudaError_t launch_layer_decode(const LayerDecodeArgs& args, const __nv_bfloat16
 
 // Shared projection with per-token low-rank adapters.
 // Up to this m, W is streamed through mma.sync; above, tcgen05 takes over
-// (4096 x 4096: 20 us against 21 at 32 tokens, 31 against 21 at 64).
+// (4096 x 4096, rank 16, 32 tokens: 18.5 us against 26.7 with one adapter, 20.6
+// against 32.9 with 32; at 64 tokens without adapters 31 against 22).
 constexpr int kLoraStreamMaxTokens = 32;
 constexpr int kLoraTileRows = 256;        // tokens of a GEMM tile
 struct LoraArgs {
