@@ -164,12 +164,12 @@ __device__ __forceinline__ bool any_bad_tile(const LoraArgs& a, int row_tiles, i
     return __any_sync(0xffffffffu, bad);
 }
 
-// SPLIT tiles with more adapters than this add them token by token while the
-// pairs' sums are joined: a stage of adapters' columns takes 1 to 2 us there
-// (128 tokens of 4096 x 4096, rank 16: 8 adapters 25 us with stages and 35 by
-// token, 64 adapters 60 and 35), a token's rows of B are read once either way.
-constexpr int kGatherAbove = 20;
-__device__ __forceinline__ bool gathers(int tile_count) { return tile_count > kGatherAbove; }
+// SPLIT tiles with more adapters than 20 per 16 rank columns add them token by
+// token while the pairs' sums are joined: the stages' time grows with the adapters
+// and the rank, a token's rows of B are read once either way.  (128 tokens of 4096
+// x 4096: rank 16, 16 adapters 33 us with stages and 35 by token, 40 40 and 37;
+// rank 32, 24 adapters 40 and 43, 64 68 and 53; rank 128, 24 adapters 90 and 154.)
+__device__ __forceinline__ bool gathers(int tile_count, int r16) { return tile_count * 16 > 20 * r16; }
 
 // more[r] = B[id of token t0 + r] row `col` . h[t0 + r] for 8 tokens (my_id: the
 // ids in lanes 0 to 7); the lanes' columns are neighbours.  Sixteen loads of B
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // from the second tile on the count is loaded ahead of the tile.
     const auto ext_steps = [&](int tile, int& first) {
         const int count = max(a.tile_count[tile / n_col_tiles], 0);
-        const int all = SPLIT && gathers(count) ? 0 : count * 2 * (a.r16 / 16);
+        const int all = SPLIT && gathers(count, a.r16) ? 0 : count * 2 * (a.r16 / 16);
         if (!SPLIT) {
             first = 0;
             return all;
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns 32 c of the tile, c = part, part + parts, ...: all pairs' partial
         // sums, in their order, 8 rows x 32 columns to a warp at a time
         const bool mend = fix[0] == tile + 1;
-        const bool by_token = gathers(a.tile_count[mt]);
+        const bool by_token = gathers(a.tile_count[mt], a.r16);
         float* buf = epi + warp * 8 * kPitch;
         static_assert(kEpiBytes >= kThreads / 32 * 8 * kPitch * 4, "a buffer per warp");
         if (!any_bad_tile(a, n_tiles / n_col_tiles, lane)) {
