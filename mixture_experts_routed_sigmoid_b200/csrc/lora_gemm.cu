@@ -933,7 +933,9 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                 dst[a.r16 / 2] = lo;
             }
         }
-        // the sums are read; the accumulator is free
+        // the sums are read; the accumulator is free (the lanes took different
+        // shares of the columns: a cluster barrier wants the warp together again)
+        __syncwarp();
         if (split > 1)
             cluster_sync();
         else
