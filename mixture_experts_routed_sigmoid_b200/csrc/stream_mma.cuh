@@ -223,7 +223,8 @@ __device__ __forceinline__ void grid_arrive(unsigned* counter) {
     }
 }
 
-// False in every thread of the block when the wait ran out (status set).
+// False in every thread of the block when the wait ran out (status set); the
+// thread's copies in flight have then landed, so that the block can leave.
 __device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned target, int* s_flag, int* status,
                                           uint64_t limit_ns) {
     if (threadIdx.x == 0) {
@@ -246,7 +247,9 @@ __device__ __forceinline__ bool grid_wait(unsigned* counter, unsigned target, in
         *s_flag = good;
     }
     __syncthreads();
-    return *s_flag != 0;
+    if (*s_flag) return true;
+    cp_async_wait_all();
+    return false;
 }
 
 }  // namespace moe
