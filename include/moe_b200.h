@@ -334,8 +334,8 @@ MOE_API moe_status_t moe_ffn_forward_shared(
  * are multiples of 8.
  * Batches that crowd more than about 8 tokens on every chosen expert are faster
  * there too (grouped GEMMs, with an fp16 activation).
- * The logits are sums in f64, rounded once to f32, so which experts are
- * chosen does not depend on the order of the additions; moe_router_topk adds
+ * The logits are sums in f64, in one order whatever m is, rounded once to f32:
+ * which experts are chosen does not depend on the batch.  moe_router_topk adds
  * in f32, and its choice can differ where two keys are that close.  The
  * activation is kept to 24 bits (three bf16 parts), the sums in f32.  NaN or
  * infinite inputs make the values that depend on them non-finite (a token's

@@ -9,9 +9,9 @@
 // expert], the definitions of moe_router_topk and moe_ffn_forward_shared.
 //
 // Kernel 1 (router): a block computes the logits of a few experts for a few
-//   tokens, its warps splitting K.  The sum is kept in f64 so that the
-//   choice of experts does not depend on the order of the additions: the
-//   rounded logits are those of the exact sum but for ties of the rounding.
+//   tokens, its warps splitting K.  The sum is kept in f64, in an order that
+//   does not depend on the batch: the rounded logits are those of the exact sum
+//   unless it lies within the f64 error of a border between two f32 values.
 // Kernel 2 (experts): a cooperative grid of one block per SM.  Every block
 //   repeats the routing of the few tokens (cheaper than a launch), takes an
 //   equal share of all active experts' gate/up rows, then, after a grid
@@ -63,6 +63,12 @@ __device__ __forceinline__ double sigmoid_f64(float v) {
 // x 8, two blocks per SM.  (256 experts of 4096, against 2 x 4 with the tokens in
 // passes: 8 tokens 4.2 us and 5.0, 32 tokens 9.7 and 13.0; 64 experts of 1024, 32
 // tokens 4.0 and 8.2.)
+// f64 additions round too, so their order is the same in every form: kSlices
+// interleaved slices of K (8 columns each), each summed in the order of K, the
+// slices of a warp in a tree over the lane's bits from the highest, the warps
+// in order.  A block of fewer threads takes its slices in passes.
+constexpr int kSlices = 512;
+
 template <int ROWS, int TOK, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_router_kernel(
     const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ W_router,
@@ -71,7 +77,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_router_
     unsigned* __restrict__ barrier, int* __restrict__ status) {
     constexpr int kSums = ROWS * TOK, kLanes = 32 / kSums;  // lanes that end with the same sum
     static_assert(kSums * kLanes == 32, "sums of a warp");
-    __shared__ double part[THREADS / 32][kSums];
+    __shared__ double part[kSlices / 32][kSums];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
         *barrier = 0;  // of the kernel that follows
@@ -85,51 +91,54 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_router_
         const int r = min(r0 + j, n_rows - 1);
         wrow[j] = r < n_experts ? W_router + static_cast<size_t>(r) * hidden : w_sh;
     }
-    double acc[kSums];
+#pragma unroll 1
+    for (int pass = 0; pass < kSlices / THREADS; ++pass) {
+        double acc[kSums];
 #pragma unroll
-    for (int i = 0; i < kSums; ++i) acc[i] = 0.0;
-    for (int k = threadIdx.x * 8; k < hidden; k += THREADS * 8) {
-        float wf[ROWS][8];
+        for (int i = 0; i < kSums; ++i) acc[i] = 0.0;
+        for (int k = (pass * THREADS + threadIdx.x) * 8; k < hidden; k += kSlices * 8) {
+            float wf[ROWS][8];
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) bf16x8_to_f32(*reinterpret_cast<const uint4*>(wrow[j] + k), wf[j]);
-        uint4 xv[TOK];
+            for (int j = 0; j < ROWS; ++j) bf16x8_to_f32(*reinterpret_cast<const uint4*>(wrow[j] + k), wf[j]);
+            uint4 xv[TOK];
 #pragma unroll
-        for (int q = 0; q < TOK; ++q)
-            xv[q] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(min(t0 + q, m - 1)) * hidden + k);
+            for (int q = 0; q < TOK; ++q)
+                xv[q] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(min(t0 + q, m - 1)) * hidden + k);
 #pragma unroll
-        for (int q = 0; q < TOK; ++q) {
-            float xf[8];
-            bf16x8_to_f32(xv[q], xf);
+            for (int q = 0; q < TOK; ++q) {
+                float xf[8];
+                bf16x8_to_f32(xv[q], xf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const double xd = xf[e];
+                for (int e = 0; e < 8; ++e) {
+                    const double xd = xf[e];
 #pragma unroll
-                for (int j = 0; j < ROWS; ++j)
-                    acc[j * TOK + q] = fma(static_cast<double>(wf[j][e]), xd, acc[j * TOK + q]);
+                    for (int j = 0; j < ROWS; ++j)
+                        acc[j * TOK + q] = fma(static_cast<double>(wf[j][e]), xd, acc[j * TOK + q]);
+                }
             }
         }
-    }
-    // the sums over 32 lanes: steps that halve the sums a lane holds (it ends
-    // with sum number lane / kLanes), then the rest
+        // the sums over 32 lanes: steps that halve the sums a lane holds (it ends
+        // with sum number lane / kLanes), then the rest
 #pragma unroll
-    for (int h = kSums / 2; h >= 1; h >>= 1) {
-        const bool upper = lane & (h * kLanes);
+        for (int h = kSums / 2; h >= 1; h >>= 1) {
+            const bool upper = lane & (h * kLanes);
 #pragma unroll
-        for (int i = 0; i < h; ++i) {
-            const double give = upper ? acc[i] : acc[i + h];
-            const double keep = upper ? acc[i + h] : acc[i];
-            acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, h * kLanes);
+            for (int i = 0; i < h; ++i) {
+                const double give = upper ? acc[i] : acc[i + h];
+                const double keep = upper ? acc[i + h] : acc[i];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, h * kLanes);
+            }
         }
-    }
 #pragma unroll
-    for (int o = kLanes / 2; o >= 1; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-    if (lane % kLanes == 0) part[warp][lane / kLanes] = acc[0];
+        for (int o = kLanes / 2; o >= 1; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        if (lane % kLanes == 0) part[pass * (THREADS / 32) + warp][lane / kLanes] = acc[0];
+    }
     __syncthreads();
     const int r = r0 + threadIdx.x / TOK, t = t0 + threadIdx.x % TOK;
     if (threadIdx.x < kSums && r < n_rows && t < m) {
         double sum = 0.0;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) sum += part[w][threadIdx.x];
+        for (int w = 0; w < kSlices / 32; ++w) sum += part[w][threadIdx.x];
         const float l = static_cast<float>(sum);
         const float s = static_cast<float>(sigmoid_f64(l));
         if (r < n_experts) {
