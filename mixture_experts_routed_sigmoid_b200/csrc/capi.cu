@@ -962,8 +962,8 @@ LoraTile lora_tile(long long m, int n, int k) {
 }
 
 // Status word, then the adapters' first products: on the streaming path the
-// partial sums h [k_splits, m, rank], for the GEMM the two bf16 parts
-// [m, 2, r16] and the adapters of each row tile.
+// partial sums h [k_splits, m, rank], for the GEMM their bf16 parts (three for
+// an f32 y, two for a bf16 one) [m, parts, r16] and the adapters of each row tile.
 struct LoraLayout {
     size_t status, h, count, list, end;
     int k_splits, r16;
@@ -979,7 +979,7 @@ LoraLayout lora_layout(long long m, int k, int rank) {
         L.h = c.take(sizeof(float) * L.k_splits * static_cast<size_t>(m) * rank);
     } else {
         const size_t tiles = static_cast<size_t>((m + moe::kLoraTileRows - 1) / moe::kLoraTileRows);
-        L.h = c.take(sizeof(uint16_t) * 2 * static_cast<size_t>(m) * L.r16);
+        L.h = c.take(sizeof(uint16_t) * 3 * static_cast<size_t>(m) * L.r16);
         L.count = c.take(sizeof(int) * tiles);
         L.list = c.take(sizeof(int) * tiles * moe::kLoraTileRows);
     }
@@ -1065,6 +1065,7 @@ MOE_API moe_status_t moe_matmul_lora(const moe_bf16_t* x, const moe_bf16_t* W,
     a.k_splits = L.k_splits;
     a.y_dtype = y_dtype;
     a.r16 = L.r16;
+    a.h_parts = y_dtype == MOE_DTYPE_F32 ? 3 : 2;
     a.wait_limit_ns = moe::kDefaultWaitLimitNs;
     cudaError_t err;
     if (stream_w) {

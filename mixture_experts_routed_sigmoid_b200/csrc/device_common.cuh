@@ -230,6 +230,19 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&f)[8]) {
     }
 }
 
+// v as the sum of three bf16 values (24 significant bits): hi = bf16(v), mid =
+// bf16(v - hi), lo = bf16(v - hi - mid).  The MMA operands of an f32 value:
+// one bf16 keeps 8 bits and two keep 16, both short of the f32 product that
+// the value stands for.  A value that is not finite is its own hi part.
+__device__ __forceinline__ void split_bf16x3(float v, __nv_bfloat16 (&p)[3]) {
+    p[0] = __float2bfloat16_rn(v);
+    const float h = __bfloat162float(p[0]);
+    const bool finite = fabsf(h) <= 3.4e38f;
+    const float r1 = finite ? v - h : 0.0f;
+    p[1] = __float2bfloat16_rn(r1);
+    p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
+}
+
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;

@@ -213,13 +213,13 @@ struct LoraArgs {
     const __nv_bfloat16* B;  // [n_adapters, n, rank]
     const float* scales;     // [n_adapters] or null
     float* h;                // streamed: [k_splits, m, rank] partial sums of A x
-    __nv_bfloat16* h_split;  // GEMM: [m, 2, r16] scales * A x as two bf16 parts
+    __nv_bfloat16* h_split;  // GEMM: [m, h_parts, r16] scales * A x as bf16 parts
     int* tile_count;         // GEMM: adapters that occur in each tile's tokens
     int* tile_list;          // GEMM: [tiles, kLoraTileRows] those adapters
     void* y;                 // [m, n]
     int* status;
     long long m;
-    int n, k, rank, r16, n_adapters, k_splits, y_dtype;
+    int n, k, rank, r16, h_parts, n_adapters, k_splits, y_dtype;
     unsigned long long wait_limit_ns;
 };
 cudaError_t launch_lora_shrink(const LoraArgs& a, int num_sms, cudaStream_t stream);

@@ -1,16 +1,17 @@
 // The projection with adapters for larger batches, in one tcgen05 GEMM:
 //   y[t] = W x[t] + B[a] (scales[a] h[t]),  a = adapter_ids[t],
-// with h = A x and its scaling from the shrink kernel, as two bf16 parts (hi,
-// lo: 16 significant bits, 2^-17 of the adapter's term; one part's 2^-9 would
-// show in an f32 y, and a third would cost half as much again).
+// with h = A x and its scaling from the shrink kernel, as bf16 parts that add up
+// to it: three for an f32 y, which keep its 24 bits (two leave an error of 2.5e-6
+// of the adapter's term, ten times that of f32 arithmetic), two for a bf16 y
+// (2^-17, below its own 2^-9).
 //
 // A CTA pair owns a tile of 256 tokens x `bn` output columns (M = 256, N = bn
 // MMAs over both CTAs; each CTA loads its 128 tokens and its half of W's rows,
 // 128 bytes of K per stage).  The adapters enter as more columns of K behind
 // the projection's: for every adapter that occurs among the tile's tokens, its
-// rank columns (rounded up to 16) twice, against the hi and the lo part of h,
-// which are zero for the tokens of other adapters.  So they cost 2 * rank / k of
-// the projection's MMAs per adapter of a tile, and no pass over y.
+// rank columns (rounded up to 16) once for each part of h, which is zero for the
+// tokens of other adapters.  So they cost parts * rank / k of the projection's
+// MMAs per adapter of a tile, and no pass over y.
 //
 // Where tiles are few (SPLIT), a cluster of 1, 2 or 4 pairs takes one tile: each
 // pair a part of K and of the adapters' stages.  The partial tiles meet in
@@ -97,7 +98,7 @@ __device__ __forceinline__ void warpgroup_sync(int warpgroup) {
 // Products of the pieces of B[adapter] row `col` that are not finite.
 __device__ __forceinline__ float fix_up(const LoraArgs& a, long long t, int id, int col) {
     const __nv_bfloat16* b = a.B + (static_cast<size_t>(id) * a.n + col) * a.rank;
-    const __nv_bfloat16* h = a.h_split + static_cast<size_t>(t) * 2 * a.r16;
+    const __nv_bfloat16* h = a.h_split + static_cast<size_t>(t) * a.h_parts * a.r16;
     float s = 0.0f;
     for (int r = 0; r < a.rank; r += 8) {
         const uint4 v = *reinterpret_cast<const uint4*>(b + r);
@@ -105,8 +106,11 @@ __device__ __forceinline__ float fix_up(const LoraArgs& a, long long t, int id, 
         float bf[8];
         bf16x8_to_f32(v, bf);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s += bf[e] * (__bfloat162float(h[r + e]) + __bfloat162float(h[a.r16 + r + e]));
+        for (int e = 0; e < 8; ++e) {
+            float hv = 0.0f;
+            for (int z = a.h_parts - 1; z >= 0; --z) hv += __bfloat162float(h[z * a.r16 + r + e]);
+            s += bf[e] * hv;
+        }
     }
     return s;
 }
@@ -164,12 +168,16 @@ __device__ __forceinline__ bool any_bad_tile(const LoraArgs& a, int row_tiles, i
     return __any_sync(0xffffffffu, bad);
 }
 
-// SPLIT tiles with more adapters than 20 per 16 rank columns add them token by
-// token while the pairs' sums are joined: the stages' time grows with the adapters
-// and the rank, a token's rows of B are read once either way.  (128 tokens of 4096
-// x 4096: rank 16, 16 adapters 33 us with stages and 35 by token, 40 40 and 37;
-// rank 32, 24 adapters 40 and 43, 64 68 and 53; rank 128, 24 adapters 90 and 154.)
-__device__ __forceinline__ bool gathers(int tile_count, int r16) { return tile_count * 16 > 20 * r16; }
+// SPLIT tiles with many adapters add them token by token while the pairs' sums
+// are joined: the stages' time grows with the adapters, the rank and the parts, a
+// token's rows of B are read once either way.  (128 tokens of 4096 x 4096, us with
+// stages and by token: rank 16, two parts, 20 adapters 34.2 and 34.9, 40 39.1 and
+// 35.3, three parts, 16 34.8 and 35.5, 20 36.9 and 35.6; rank 32, two, 24 39.8 and
+// 41.9, 40 47.4 and 43.8, three, 16 39.5 and 41.7, 24 44.7 and 42.5; rank 128,
+// two, 24 84.8 and 137, 64 195 and 198, three, 24 108 and 138, 64 255 and 199.)
+__device__ __forceinline__ bool gathers(const LoraArgs& a, int tile_count) {
+    return tile_count * a.h_parts > 36 + 12 * (a.r16 / 16);
+}
 
 // more[r] = B[id of token t0 + r] row `col` . h[t0 + r] for 8 tokens (my_id: the
 // ids in lanes 0 to 7); the lanes' columns are neighbours.  Sixteen loads of B
@@ -185,18 +193,18 @@ __device__ __forceinline__ void gather_rows(const LoraArgs& a, float (&more)[8],
     }
     const bool in = col < a.n;
     const int h_token = lane >> 2, h_id = __shfl_sync(0xffffffffu, my_id, h_token);
-    const __nv_bfloat16* h_row = a.h_split + (t0 + (h_id >= 0 ? h_token : 0)) * 2 * a.r16 + (lane & 3) * 8;
+    const __nv_bfloat16* h_row = a.h_split + (t0 + (h_id >= 0 ? h_token : 0)) * a.h_parts * a.r16 + (lane & 3) * 8;
     for (int k0 = 0; k0 < a.rank; k0 += 32) {
         float h[8];
         const bool h_in = h_id >= 0 && k0 + (lane & 3) * 8 < a.rank;
-        {
-            const uint4 hi = h_in ? *reinterpret_cast<const uint4*>(h_row + k0) : make_uint4(0u, 0u, 0u, 0u);
-            const uint4 lo = h_in ? *reinterpret_cast<const uint4*>(h_row + a.r16 + k0) : make_uint4(0u, 0u, 0u, 0u);
-            float fl[8];
-            bf16x8_to_f32(hi, h);
-            bf16x8_to_f32(lo, fl);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] += fl[e];
+        for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+        for (int z = a.h_parts - 1; z >= 0; --z) {
+            float part[8];
+            bf16x8_to_f32(h_in ? *reinterpret_cast<const uint4*>(h_row + z * a.r16 + k0) : make_uint4(0u, 0u, 0u, 0u),
+                          part);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] += part[e];
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // from the second tile on the count is loaded ahead of the tile.
     const auto ext_steps = [&](int tile, int& first) {
         const int count = max(a.tile_count[tile / n_col_tiles], 0);
-        const int all = SPLIT && gathers(count, a.r16) ? 0 : count * 2 * (a.r16 / 16);
+        const int all = SPLIT && gathers(a, count) ? 0 : count * a.h_parts * (a.r16 / 16);
         if (!SPLIT) {
             first = 0;
             return all;
@@ -380,43 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int tile = cluster; tile < n_tiles && good; tile += n_clusters, ++seq) {
                     uint32_t d = 0;
                     int first, steps = tile == cluster ? 0 : ext_steps(tile, first);
-                    bool ready = false;
-                    int in_chunk = chunk;  // stages that the accumulator has
-                    for (int kb = 0; kb < nk; ++kb, ++in_chunk) {
-                        if (in_chunk == chunk) {
-                            if (kb > 0) finish_chunk();
-                            in_chunk = 0;
-                            good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
-                            if (!good) break;
-                            tc_fence_after_sync();
-                            d = tmem + static_cast<uint32_t>(acc * 256);
-                        }
-                        good = __all_sync(0xffffffffu, ready || mbar_wait(&full[stage], phase, ctl));
-                        if (!good) break;
-                        tc_fence_after_sync();
-                        const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
-                        uint64_t* done = &empty[stage];
-                        advance(stage, phase);
-                        // the next stage's barrier is asked while these MMAs are issued
-                        if (kb + 1 < nk) ready = mbar_test(&full[stage], phase);
-                        if (leader) {
-#pragma unroll
-                            for (int k4 = 0; k4 < 4; ++k4)
-                                umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
-                                               (in_chunk | k4) != 0);
-                            umma_commit_pair(done, lead);
-                        }
-                        __syncwarp();
-                    }
-                    if (!good) break;
-                    if (tile == cluster) {
-                        wait_for_previous_kernel();
-                        steps = ext_steps(tile, first);
-                    }
-                    for (int left = steps; left > 0; left -= 4, ++n) {
-                        const int e = n % kExt;
-                        good = __all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl));
-                        if (!good) break;
+                    // The adapters' stages are spread evenly over the projection's, so
+                    // that the copies of those beyond the two buffers have their time
+                    // (16384 tokens of rank 64, three stages a tile: 286 us, 319 with all
+                    // at the end); those of the first tile follow it.
+                    int ext = 0, ext_all = (steps + 3) / 4;
+                    const auto adapter_stage = [&]() -> bool {
+                        const int e = n % kExt, left = steps - 4 * ext;
+                        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&ext_full[e], n / kExt & 1u, ctl))) return false;
                         tc_fence_after_sync();
                         const uint64_t da = desc0 + static_cast<uint64_t>((n_stages + e) * (stage_size >> 4));
                         if (bad_ext[e] && lane == 0) {
@@ -432,6 +411,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_commit_pair(&ext_empty[e], lead);
                         }
                         __syncwarp();
+                        ++ext, ++n;
+                        return true;
+                    };
+                    bool ready = false;
+                    int in_chunk = chunk;  // stages that the accumulator has
+                    int kb = 0;
+                    bool waited = tile != cluster;
+                    for (;;) {
+                        const int stop = ext < ext_all ? ((ext + 1) * nk + ext_all - 1) / ext_all : nk;
+                        for (; kb < stop; ++kb, ++in_chunk) {
+                            if (in_chunk == chunk) {
+                                if (kb > 0) finish_chunk();
+                                in_chunk = 0;
+                                good = __all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[acc], acc_phase ^ 1, ctl));
+                                if (!good) break;
+                                tc_fence_after_sync();
+                                d = tmem + static_cast<uint32_t>(acc * 256);
+                            }
+                            good = __all_sync(0xffffffffu, ready || mbar_wait(&full[stage], phase, ctl));
+                            if (!good) break;
+                            tc_fence_after_sync();
+                            const uint64_t da = desc0 + static_cast<uint64_t>(stage * (stage_size >> 4));
+                            uint64_t* done = &empty[stage];
+                            advance(stage, phase);
+                            // the next stage's barrier is asked while these MMAs are issued
+                            if (kb + 1 < nk) ready = mbar_test(&full[stage], phase);
+                            if (leader) {
+#pragma unroll
+                                for (int k4 = 0; k4 < 4; ++k4)
+                                    umma_bf16_pair(d, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
+                                                   (in_chunk | k4) != 0);
+                                umma_commit_pair(done, lead);
+                            }
+                            __syncwarp();
+                        }
+                        if (good && kb == nk && !waited) {
+                            wait_for_previous_kernel();
+                            steps = ext_steps(tile, first);
+                            ext_all = (steps + 3) / 4;
+                            waited = true;
+                        }
+                        if (!good || ext == ext_all) break;
+                        if (!(good = adapter_stage())) break;
                     }
                     if (!good) break;
                     finish_chunk();
@@ -485,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pt = tid - 256, piece = pt & 7, row0 = pt >> 3;
             const uint32_t ext = smem_u32(smem) + static_cast<uint32_t>(row0 * 128 + ((piece ^ (row0 & 7)) << 4));
             const size_t b_adapter = static_cast<size_t>(a.n) * a.rank;
+            const int h_pitch = a.h_parts * a.r16;
             int n = 0;
             bool good = true;
             for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
@@ -501,24 +524,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) id[i] = t0 + 16 * i < a.m ? a.adapter_ids[t0 + 16 * i] : -1;
                 // this thread's column among the adapters': adapter of the list and
-                // column within its 2 * r16
+                // column within its parts
                 int first;
                 const int steps = ext_steps(tile, first);
-                int ad = (first * 16 + piece * 8) / (2 * a.r16), rem = first * 16 + piece * 8 - ad * 2 * a.r16;
+                int ad = (first * 16 + piece * 8) / h_pitch, rem = first * 16 + piece * 8 - ad * h_pitch;
                 for (int left = steps; left > 0; left -= 4, ++n) {
                     const int e = n % kExt;
                     if (!(good = mbar_wait_cluster(&ext_empty[e], (n / kExt & 1u) ^ 1u, ctl))) break;
                     const uint32_t sa = ext + static_cast<uint32_t>((n_stages + e) * stage_size);
                     const bool in = ad < count;
                     const int adapter = in ? list[ad] : 0;
-                    const int r = rem < a.r16 ? rem : rem - a.r16;
+                    int r = rem;  // column of the rank
+                    while (r >= a.r16) r -= a.r16;
                     const bool b_in = in && r < a.rank;
-                    const __nv_bfloat16* h = a.h_split + t0 * 2 * a.r16 + rem;
+                    const __nv_bfloat16* h = a.h_split + t0 * h_pitch + rem;
                     const __nv_bfloat16* b = a.B + adapter * b_adapter + static_cast<size_t>(col0) * a.rank + r;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const bool use = in && id[i] == adapter;
-                        cp_async_16(sa + i * 16 * 128, use ? h + i * 32 * a.r16 : a.h_split, use ? 16u : 0u);
+                        cp_async_16(sa + i * 16 * 128, use ? h + i * 16 * h_pitch : a.h_split, use ? 16u : 0u);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -527,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         cp_async_16(sa + kHalf + i * 16 * 128, use ? b + i * 16 * a.rank : a.B, use ? 16u : 0u);
                     }
                     cp_async_arrive_noinc(&landed[e]);
-                    for (rem += 64; rem >= 2 * a.r16; rem -= 2 * a.r16) ++ad;
+                    for (rem += 64; rem >= h_pitch; rem -= h_pitch) ++ad;
                 }
             }
             cp_async_wait_all();
@@ -631,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns 32 c of the tile, c = part, part + parts, ...: all pairs' partial
         // sums, in their order, 8 rows x 32 columns to a warp at a time
         const bool mend = fix[0] == tile + 1;
-        const bool by_token = gathers(a.tile_count[mt], a.r16);
+        const bool by_token = gathers(a, a.tile_count[mt]);
         float* buf = epi + warp * 8 * kPitch;
         static_assert(kEpiBytes >= kThreads / 32 * 8 * kPitch * 4, "a buffer per warp");
         if (!any_bad_tile(a, n_tiles / n_col_tiles, lane)) {
@@ -912,25 +936,14 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                         v[1] = own[1];
                     }
                 }
-                // hi + lo: 16 significant bits; a value that is not finite is its own hi part
-                __nv_bfloat162 hi, lo;
+                __nv_bfloat16 p0[3], p1[3];
+                split_bf16x3(v[0] * scale, p0);
+                split_bf16x3(v[1] * scale, p1);
+                __nv_bfloat16* dst = a.h_split + (t0 + row) * a.h_parts * a.r16 + r;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float x = v[i] * scale;
-                    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-                    const float hf = __bfloat162float(h);
-                    const __nv_bfloat16 l = __float2bfloat16_rn(fabsf(hf) <= 3.4e38f ? x - hf : 0.0f);
-                    if (i == 0) {
-                        hi.x = h;
-                        lo.x = l;
-                    } else {
-                        hi.y = h;
-                        lo.y = l;
-                    }
-                }
-                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.h_split + (t0 + row) * 2 * a.r16 + r);
-                dst[0] = hi;
-                dst[a.r16 / 2] = lo;
+                for (int z = 0; z < 3; ++z)
+                    if (z < a.h_parts)
+                        *reinterpret_cast<__nv_bfloat162*>(dst + z * a.r16) = __nv_bfloat162(p0[z], p1[z]);
             }
         }
         // the sums are read; the accumulator is free (the lanes took different

@@ -197,19 +197,6 @@ __device__ __forceinline__ void ring_multiply_one(float (&acc)[2][NT][4], uint32
     }
 }
 
-// v as the sum of three bf16 values (24 significant bits): hi = bf16(v), mid =
-// bf16(v - hi), lo = bf16(v - hi - mid).  The MMA operands of an f32 value:
-// one bf16 keeps 8 bits and two keep 16, both short of the f32 product that
-// the value stands for.  A value that is not finite is its own hi part.
-__device__ __forceinline__ void split_bf16x3(float v, __nv_bfloat16 (&p)[3]) {
-    p[0] = __float2bfloat16_rn(v);
-    const float h = __bfloat162float(p[0]);
-    const bool finite = fabsf(h) <= 3.4e38f;
-    const float r1 = finite ? v - h : 0.0f;
-    p[1] = __float2bfloat16_rn(r1);
-    p[2] = __float2bfloat16_rn(r1 - __bfloat162float(p[1]));
-}
-
 // Grid-wide barrier of a cooperative launch: every block's writes before
 // grid_arrive are visible to every block after its grid_wait.  `counter` is
 // zero before the launch; the n-th barrier of a kernel waits for target = n *

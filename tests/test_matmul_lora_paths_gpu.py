@@ -42,3 +42,27 @@ def check(c, got):
 def test_first_product_in_several_passes(m, n, k, rank, D):
     c = make(m, n, k, rank, D, lambda t: (t * 7) % (D + 1) - 1)
     check(c, call(c))
+
+
+@pytest.mark.parametrize("m, n, D", [
+    (20, 100, 5),                 # streamed
+    (33, 100, 5), (200, 700, 3),  # joined tiles
+    (200, 700, 120),              # joined, the adapters' part token by token
+    (5000, 2100, 3),              # several tiles to a CTA pair
+])
+def test_an_f32_output_keeps_all_bits_of_the_first_product(m, n, D):
+    """Whole numbers: A x has up to 21 bits, every sum of it is below 2^24, and a
+    row of B picks one of its columns, so that y is A x exactly or has lost bits."""
+    k, rank = 512, 16
+    g = torch.Generator(device="cuda").manual_seed(m + D)
+    whole = lambda top, *shape: torch.randint(-top, top + 1, shape, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, A = whole(255, m, k), whole(127, D, rank, k)
+    B = torch.zeros(D, n, rank, device="cuda")
+    B[:, torch.arange(n), torch.arange(n) % rank] = 1.0
+    ids = (torch.arange(m, device="cuda") % (D + 1) - 1).int()
+    scales = 2.0 ** torch.randint(-3, 4, (D,), generator=g, device="cuda")
+    c = {"x": x, "W": torch.zeros(n, k, device="cuda").bfloat16(), "A": A, "B": B.bfloat16(), "ids": ids, "scales": scales}
+    h = torch.einsum("tk,drk->tdr", x.double(), A.double())[torch.arange(m), ids.long().clamp(min=0)]
+    assert 2 ** 18 < h.abs().max() < 2 ** 23
+    want = torch.where(ids[:, None] >= 0, h[:, torch.arange(n) % rank] * scales.double()[ids.long().clamp(min=0), None], 0.0)
+    assert torch.equal(call(c).double(), want)
