@@ -3,7 +3,7 @@
 // with h = A x and its scaling from the shrink kernel, as bf16 parts that add up
 // to it: three for an f32 y, which keep its 24 bits (two leave an error of 2.5e-6
 // of the adapter's term, ten times that of f32 arithmetic), two for a bf16 y
-// (2^-17, below its own 2^-9).
+// (2^-17, below its own 2^-8).
 //
 // A CTA pair owns a tile of 256 tokens x `bn` output columns (M = 256, N = bn
 // MMAs over both CTAs; each CTA loads its 128 tokens and its half of W's rows,
@@ -786,7 +786,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.stages * lay.stage);
     uint64_t* empty = full + kShrinkMaxStages;
     uint64_t* acc_full = empty + kShrinkMaxStages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* acc_empty = acc_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* sums = reinterpret_cast<float*>(smem + lay.stages * lay.stage + 256);  // [128][pitch]
     __shared__ __align__(16) int s_id[kLoraTileRows];
@@ -802,6 +803,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 4);  // the warps that read the accumulators
         *abort_flag = 0;
         s_bad = 0;
         fence_barrier_init();
@@ -834,9 +836,11 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
 
     const int nkb = (a.k + 63) / 64;
     const int kb_lo = nkb * rank / split, kb_hi = nkb * (rank + 1) / split;
-    // for an f32 output up to four accumulators of 8 stages (more where K is
-    // longer) each, against the tensor core's truncation (see the projection)
-    const int n_kb = kb_hi - kb_lo, n_sums = a.y_dtype == MOE_DTYPE_F32 ? min((n_kb + 7) / 8, 4) : 1;
+    // Against the tensor core's truncation (see the projection), a round of up to
+    // four accumulators of at most kChunk stages, and as many rounds as K takes.
+    const int n_kb = kb_hi - kb_lo, rounds = (n_kb + 4 * kChunk - 1) / (4 * kChunk);
+    const auto round_begin = [&](int round) { return kb_lo + n_kb * round / rounds; };
+    const auto accumulators = [](int n) { return min((n + 7) / 8, 4); };
     int stage = 0;
     uint32_t phase = 0, acc_phase = 0;
     const auto advance = [&] {
@@ -865,47 +869,63 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
             const uint32_t idesc = umma_idesc_bf16_f32(128, here * a.r16);
             const bool leader = elect_one();
             bool good = true;
-            for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
+            for (int round = 0; round < rounds && good; ++round) {
+                const int lo = round_begin(round), n = round_begin(round + 1) - lo, n_sums = accumulators(n);
+                good = __all_sync(0xffffffffu, mbar_wait(acc_empty, acc_phase ^ 1, ctl));
                 if (!good) break;
                 tc_fence_after_sync();
-                const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
-                const int q = (kb - kb_lo) * n_sums / n_kb;
-                const bool more = kb > kb_lo && (kb - 1 - kb_lo) * n_sums / n_kb == q;
-                if (leader) {
+                int q = 0, next_q = 0;  // this stage's accumulator; the stage where it is the next one's turn
+                for (int i = 0; i < n; ++i) {
+                    good = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase, ctl));
+                    if (!good) break;
+                    tc_fence_after_sync();
+                    const uint64_t da = desc0 + static_cast<uint64_t>(stage * (lay.stage >> 4));
+                    const bool first = i == next_q;
+                    if (first) {
+                        q = i * n_sums / n;
+                        next_q = ((q + 1) * n + n_sums - 1) / n_sums;
+                    }
+                    if (leader) {
 #pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4)
-                        umma_bf16(tmem + q * MOE_MAX_LORA_RANK, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
-                                  more || k4 > 0);
-                    umma_commit(&empty[stage]);
+                        for (int k4 = 0; k4 < 4; ++k4)
+                            umma_bf16(tmem + q * MOE_MAX_LORA_RANK, da + k4 * 2, da + (kHalf >> 4) + k4 * 2, idesc,
+                                      !first || k4 > 0);
+                        umma_commit(&empty[stage]);
+                    }
+                    __syncwarp();
+                    advance();
                 }
+                if (good && leader) umma_commit(acc_full);
                 __syncwarp();
-                advance();
+                acc_phase ^= 1;
             }
-            if (good && leader) umma_commit(acc_full);
-            __syncwarp();
         } else if (warp >= 4) {
-            const bool good = __all_sync(0xffffffffu, mbar_wait(acc_full, acc_phase, ctl));
-            tc_fence_after_sync();
-            if (good)
+            for (int round = 0; round < rounds; ++round) {
+                if (!__all_sync(0xffffffffu, mbar_wait(acc_full, acc_phase, ctl))) break;
+                tc_fence_after_sync();
+                const int n_sums = accumulators(round_begin(round + 1) - round_begin(round));
                 for (int c = 0; c < (here * a.r16 + 31) / 32; ++c) {
+                    float* row = sums + ((warp & 3) * 32 + lane) * pitch + c * 32;
                     float sum[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[i] = round > 0 && c * 32 + i < cols ? row[i] : 0.0f;
                     for (int q = 0; q < n_sums; ++q) {
                         uint32_t v[32];
                         tmem_load_32cols(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
                                              q * MOE_MAX_LORA_RANK + c * 32, v);
                         tmem_load_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            sum[i] = q == 0 ? __uint_as_float(v[i]) : sum[i] + __uint_as_float(v[i]);
+                        for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
                     }
-                    float* row = sums + ((warp & 3) * 32 + lane) * pitch + c * 32;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (c * 32 + i < cols) row[i] = sum[i];
                 }
-            tc_fence_before_sync();
-            acc_phase ^= 1;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty);
+                acc_phase ^= 1;
+            }
         }
         __syncwarp();
         if (split > 1)
@@ -946,8 +966,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1)
                         *reinterpret_cast<__nv_bfloat162*>(dst + z * a.r16) = __nv_bfloat162(p0[z], p1[z]);
             }
         }
-        // the sums are read; the accumulator is free (the lanes took different
-        // shares of the columns: a cluster barrier wants the warp together again)
+        // the sums are read (the lanes took different shares of the columns: a
+        // cluster barrier wants the warp together again)
         __syncwarp();
         if (split > 1)
             cluster_sync();

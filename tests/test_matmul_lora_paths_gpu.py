@@ -66,3 +66,30 @@ def test_an_f32_output_keeps_all_bits_of_the_first_product(m, n, D):
     assert 2 ** 18 < h.abs().max() < 2 ** 23
     want = torch.where(ids[:, None] >= 0, h[:, torch.arange(n) % rank] * scales.double()[ids.long().clamp(min=0), None], 0.0)
     assert torch.equal(call(c).double(), want)
+
+
+@pytest.mark.parametrize("m, k", [(8, 2 ** 18), (200, 2 ** 20), (1100, 2 ** 18)])
+def test_the_first_product_of_a_long_k(m, k):
+    """The tensor core truncates: an instruction loses up to 2^-23 of its sum, 48
+    of them (768 columns) at most 96 u of a partial sum, u = 2^-24.  The errors of
+    the partial sums are independent: in the 2-norm 96 u of the whole, and their
+    additions round, sqrt(k / 768) u of it.  (One sum of 32768 columns would be off
+    by 4e-5.)  x and A are random, the projection is zero, B picks columns of A x."""
+    n, rank, D = 48, 16, 2
+    g = torch.Generator(device="cuda").manual_seed(m)
+    c = {"x": normal(g, m, k), "W": torch.zeros(n, k, device="cuda").bfloat16(), "A": normal(g, D, rank, k, std=k ** -0.5),
+         "ids": (torch.arange(m, device="cuda") % D).int(), "scales": None}
+    B = torch.zeros(D, n, rank, device="cuda")
+    B[:, torch.arange(n), torch.arange(n) % rank] = 1.0
+    c["B"] = B.bfloat16()
+    h = sum(torch.einsum("tk,drk->tdr", c["x"][:, i:i + 2 ** 16].double(), c["A"][:, :, i:i + 2 ** 16].double())
+            for i in range(0, k, 2 ** 16))[torch.arange(m), c["ids"].long()]
+    want = h[:, torch.arange(n) % rank]
+    y = call(c).double()
+    off = ((y - want).norm() / want.norm()).item()
+    assert off <= (96 + (k / 768) ** 0.5) * ref.U, off
+    # a bf16 output rounds by at most 2^-8 of its value, A x by 2^-17, and each of the k / 768
+    # partial sums, about sqrt(768 / k) of x's size, loses at most 96 u
+    y = call(c, out_dtype=torch.bfloat16).double()
+    more = (y - want).abs() - (2.0 ** -8 + 2.0 ** -17) * want.abs()
+    assert (more <= 96 * ref.U * (k / 768) ** 0.5 * c["x"].double().square().mean().sqrt()).all()
