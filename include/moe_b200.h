@@ -378,9 +378,9 @@ MOE_API moe_status_t moe_layer_decode(
  * can depend on m and on which adapters the other tokens have (they decide how
  * K is split and how the adapters' part is added); the same call gives the
  * same bits.  Sums are f32 ones.  Above 32 tokens they are taken from the tensor
- * core every 768 columns of k where y is f32, and scales * A x is kept to 24 bits
- * where y is f32 and to 16 where it is bf16, |error| <= 2^-17 of it (a value above
- * bf16's largest becomes infinite).
+ * core every 768 columns of k (1024 where y is bf16), and scales * A x is kept to
+ * 24 bits where y is f32 and to 16 where it is bf16, |error| <= 2^-17 of it (a
+ * value above bf16's largest becomes infinite).
  * An id out of range sets MOE_ERR_DEVICE_BAD_ID in the ws status word
  * (moe_check_status) and leaves y unwritten.
  */

@@ -49,7 +49,8 @@ constexpr int kMaxStages = 8;         // ring of the projection's stages
 constexpr int kExt = 2;               // stages of the adapters' columns, beside the ring
 constexpr int kHalf = 128 * 128;      // bytes of 128 rows x 64 columns
 constexpr int kThreads = 512;
-constexpr int kChunk = 12;            // stages of the projection per accumulator, at most (f32 output)
+constexpr int kChunk = 12;            // stages per accumulator, at most (f32 output, first product)
+constexpr int kChunkBf16 = 16;        // and of the projection for a bf16 output
 constexpr int kTmemCols = 512;
 constexpr int kFixSlots = 4;
 constexpr int kPartPitch = 36;        // words of a partial tile's row of 32 columns
@@ -301,14 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nk_all = (a.k + 63) / 64, kb_lo = nk_all * part / parts;
     const int nk = nk_all * (part + 1) / parts - kb_lo;  // this pair's stages of the projection
     const int half = bn / 2;
-    // The tensor core's accumulator truncates: over K = 2048 its sums are off by
-    // 2.1e-6 of their size, over 16384 by 1.9e-5, where additions that round are off
-    // by 5e-7.  So an f32 output's sums are taken from it every 768 columns of K
-    // and added in registers (6.5e-7 at every K).  A bf16 output rounds by 2^-9
-    // and takes them once.  (16384 tokens of 2048 x 4096: 242 us without, 250
-    // with 768 columns, 261 with 512: the two accumulators then hold too little
-    // work to cover the stores of a tile.)
-    const int chunk = a.y_dtype == MOE_DTYPE_F32 ? kChunk : nk, n_chunks = (nk + chunk - 1) / chunk;
+    // The tensor core's accumulator truncates: its sums over K are off by 1e-9 K of
+    // their size (2.1e-6 at 2048, 1.9e-5 at 16384), where additions that round are
+    // off by 5e-7.  So they are taken from it every 768 columns of K for an f32
+    // output (6.5e-7 at every K), every 1024 for a bf16 one, and added in registers.
+    // (16384 tokens of 2048 x 4096, f32: 242 us without, 250 with 768 columns, 261
+    // with 512: the two accumulators then hold too little work to cover the stores
+    // of a tile.  4096 tokens of 4096 x 4096, bf16: 120.5 us without, 122.5 with
+    // 1024 columns, 126 with 768; 2.4, 0.7 and 0.5 of 1000 values are then not the
+    // rounding of the exact one, of sums in f32 arithmetic 0.4.)
+    const int chunk = a.y_dtype == MOE_DTYPE_F32 ? kChunk : kChunkBf16, n_chunks = (nk + chunk - 1) / chunk;
     // MMA steps (16 columns of K) of the adapters of a tile.  The shrink kernel
     // must have finished: waited for behind the first tile's projection, and
     // from the second tile on the count is loaded ahead of the tile.

@@ -93,3 +93,24 @@ def test_the_first_product_of_a_long_k(m, k):
     y = call(c, out_dtype=torch.bfloat16).double()
     more = (y - want).abs() - (2.0 ** -8 + 2.0 ** -17) * want.abs()
     assert (more <= 96 * ref.U * (k / 768) ** 0.5 * c["x"].double().square().mean().sqrt()).all()
+
+
+@pytest.mark.parametrize("m, n, k", [
+    (20, 64, 2 ** 17),            # streamed
+    (40, 64, 2 ** 18),            # K over four CTA pairs
+    (2000, 2400, 2 ** 15),        # a tile or two to a CTA pair, each its whole K
+])
+def test_a_bf16_output_of_a_long_k_is_the_rounding_of_its_sum(m, n, k):
+    """All products are positive, so that the tensor core's truncation (up to 2^-23
+    = 2 u of the sum per instruction of 16 products) adds up: by 128 u of a partial
+    sum of 1024 columns, and the k / 1024 additions of partial sums, which round,
+    by u of the whole each.  What is left is the output's half step.  (A sum over
+    all of K lost up to k / 8 u, 2^-9 at k = 2^18.)"""
+    g = torch.Generator(device="cuda").manual_seed(m)
+    c = {"x": normal(g, m, k).abs(), "W": normal(g, n, k, std=1 / k).abs(), "scales": None,
+         "A": torch.zeros(1, 8, k, device="cuda").bfloat16(), "B": torch.zeros(1, n, 8, device="cuda").bfloat16(),
+         "ids": torch.full((m,), -1, dtype=torch.int32, device="cuda")}
+    want = sum(c["x"][:, i:i + 2 ** 13].double() @ c["W"][:, i:i + 2 ** 13].double().T for i in range(0, k, 2 ** 13))
+    y = call(c, out_dtype=torch.bfloat16).double()
+    step = 2.0 ** (torch.floor(torch.log2(want)) - 7)
+    assert ((y - want).abs() <= step / 2 + (128 + k / 1024) * ref.U * want).all()
