@@ -114,3 +114,138 @@ def test_a_bf16_output_of_a_long_k_is_the_rounding_of_its_sum(m, n, k):
     y = call(c, out_dtype=torch.bfloat16).double()
     step = 2.0 ** (torch.floor(torch.log2(want)) - 7)
     assert ((y - want).abs() <= step / 2 + (128 + k / 1024) * ref.U * want).all()
+
+
+def varied_ids(m, D, seed):
+    """Row tiles of 256 tokens without an adapter, with one, with a few in runs, with all."""
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.empty(m, dtype=torch.int64)
+    for at in range(0, m, 256):
+        n, kind = min(256, m - at), at // 256 % 4
+        ids[at:at + n] = (torch.full((n,), -1) if kind == 0 else torch.full((n,), at % D) if kind == 1
+                          else (torch.arange(n) // 50 + at) % D if kind == 2 else torch.randint(-1, D, (n,), generator=g))
+    return ids.tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m, n, k, rank, D", [
+    (5000, 4100, 1000, 24, 7),    # 20 x 17 tiles of 256 x 256 or more of fewer columns
+    (4700, 4100, 264, 128, 5),    # more columns of adapters than of k
+    (9000, 2500, 72, 8, 40),
+])
+def test_row_tiles_one_after_another(m, n, k, rank, D, dtype):
+    """Several tiles to each of the 74 CTA pairs, whose adapters differ in number:
+    barriers, adapter lists and the adapters' buffers go from tile to tile."""
+    assert -(-m // 256) * -(-n // 256) > 4 * 74
+    c = make(m, n, k, rank, D, varied_ids(m, D, m))
+    y = torch.full((m + 1, n), -7777.0, dtype=dtype, device="cuda")
+    check(c, call(c, y=y[:m]))
+    assert (y[m:] == -7777.0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_a_broken_adapter_of_many_row_tiles(dtype, bad):
+    """B of one adapter is not finite in some columns, x in a row: the other
+    values keep their bits."""
+    m, n, k, rank, D = 5000, 4100, 264, 24, 7
+    c = make(m, n, k, rank, D, varied_ids(m, D, 3))
+    want = call(c, out_dtype=dtype)
+    columns = torch.tensor([0, 31, 200, 1777, 4099], device="cuda")
+    d = dict(c, B=c["B"].clone())
+    d["B"][2, columns, rank - 1] = bad
+    got = call(d, out_dtype=dtype)
+    hit = c["ids"] == 2
+    assert hit.any() and not torch.isfinite(got[hit][:, columns]).any()
+    got[:, columns] = torch.where(hit[:, None], want[:, columns], got[:, columns])
+    assert torch.equal(got, want)
+    d = dict(c, x=c["x"].clone())
+    d["x"][4444, 5] = bad
+    got = call(d, out_dtype=dtype)
+    assert not torch.isfinite(got[4444]).any()
+    got[4444] = want[4444]
+    assert torch.equal(got, want)
+
+
+BY_TOKEN = [
+    # m, n, k, rank: one tile per cluster, of 1, 2 or 4 CTA pairs
+    (65, 513, 256, 32), (251, 700, 512, 16),
+    (200, 1300, 2048, 40), (90, 1000, 2048, 16),
+    (150, 520, 4096, 24), (47, 300, 4096, 8), (200, 2300, 1024, 128), (300, 520, 2048, 16), (250, 4000, 2048, 16),
+    (260, 2300, 2048, 40),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("D", [15, 17, 21, 25, 31, 37, 45, 70, 250])
+@pytest.mark.parametrize("m, n, k, rank", BY_TOKEN)
+def test_numbers_of_adapters_around_the_by_token_border(m, n, k, rank, D, dtype):
+    c = make(m, n, k, rank, D, lambda t: (t * 3) % (D + 1) - 1, seed=D)
+    check(c, call(c, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("m, n, k, rank", BY_TOKEN)
+def test_a_broken_adapter_by_token(m, n, k, rank, bad):
+    D = 200
+    c = make(m, n, k, rank, D, lambda t: (t * 3) % (D + 1) - 1)
+    want = call(c)
+    a = c["ids"][m // 2].item()
+    hit = c["ids"] == a
+    for part in ("A", "B"):
+        d = dict(c, **{part: c[part].clone()})
+        d[part][a] = bad
+        got = call(d)
+        assert torch.equal(got[~hit], want[~hit]) and not torch.isfinite(got[hit]).any()
+    d = dict(c, B=c["B"].clone())
+    d["B"][a, 7, rank - 1] = bad
+    got = call(d)
+    assert not torch.isfinite(got[hit][:, 7]).any()
+    got[hit, 7] = want[hit, 7]
+    assert torch.equal(got, want)
+    d = dict(c, x=c["x"].clone())
+    d["x"][5] = bad
+    got = call(d)
+    assert not torch.isfinite(got[5]).any()
+    got[5] = want[5]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m, k, rank, D", [(32, 1024, 128, 32), (32, 4096, 120, 40), (29, 72, 128, 29)])
+def test_streamed_adapters_beyond_a_block_each(m, k, rank, D):
+    """Eight blocks of 16 rank rows to an adapter leave 18 adapters at once."""
+    c = make(m, 300, k, rank, D, lambda t: t % D)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("m, n, k, rank, D", [(33, 1, 8, 8, 1), (40, 24, 8, 128, 3), (257, 1, 24, 8, 2), (256, 7, 16, 16, 1)])
+def test_smallest_sizes_of_larger_batches(m, n, k, rank, D):
+    c = make(m, n, k, rank, D, lambda t: t % (D + 1) - 1)
+    check(c, call(c))
+    check(c, call(c, out_dtype=torch.bfloat16))
+
+
+def test_adapters_past_32_bit_offsets():
+    """A and B of more than 2^31 values each; the adapters that no token uses hold whatever was there."""
+    n, k, rank, D = 4096, 4096, 16, 33000
+    assert D * rank * k > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    used = [0, 20000, D - 1]
+    A, B = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((D, rank, k), (D, n, rank)))
+    for a in used:
+        A[a], B[a] = normal(g, rank, k, std=k ** -0.5), normal(g, n, rank, std=0.25)
+    for m in (20, 100, 2500):
+        pick = torch.arange(m, device="cuda") % 4 - 1
+        c = {"x": normal(g, m, k), "W": normal(g, n, k, std=k ** -0.5), "A": A[used], "B": B[used], "scales": None, "ids": pick.int()}
+        ids = torch.where(pick >= 0, torch.tensor(used, device="cuda")[pick.clamp(min=0)], -1).int()
+        check(c, moe.moe_matmul_lora(c["x"], c["W"], ids, A, B))
+
+
+def test_rows_past_32_bit_offsets():
+    m, n, k, rank, D = 263000, 8200, 64, 8, 3
+    assert m * n > 2 ** 31
+    c = make(m, n, k, rank, D, lambda t: t % (D + 1) - 1)
+    y = call(c, out_dtype=torch.bfloat16)
+    for at in (0, 131072, 261888, m - 300):
+        rows = slice(at, at + 300)
+        check(dict(c, x=c["x"][rows], ids=c["ids"][rows]), y[rows])
