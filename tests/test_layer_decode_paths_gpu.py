@@ -48,3 +48,55 @@ def test_logits_have_the_same_bits_in_every_batch(hidden):
     for m in (1, 4, 5, 8, 9, 16, 17):
         part = call(dict(c, x=c["x"][:m].contiguous()))[3]
         assert torch.equal(part, whole[:m])
+
+
+def check(c, got):
+    cpu = lambda t: None if t is None else t.cpu()  # noqa: E731
+    y, bound, ids, w, logits = ref.layer(cpu(c["x"]), cpu(c["W_router"]), cpu(c["bias"]), c["top_k"], cpu(c["W_gate"]),
+                                         cpu(c["W_up"]), cpu(c["W_down"]), tuple(map(cpu, c["shared"])) or None)
+    gy, gids, gw, gl = map(cpu, got)
+    # f64 sums rounded once: the exact sum's rounding but for ties, one step apart at most
+    assert ((gl.double() - logits.double()).abs() <= 2 * ref.U * logits.double().abs() + ref.TINY).all()
+    assert torch.equal(gids.long(), ids)
+    assert ((gw.double() - w).abs() <= 2 * ref.U * w).all()
+    off = (gy.double() - y).abs()
+    assert (off <= bound).all(), f"worst {(off / bound).max():.3g} of the bound"
+
+
+@pytest.mark.parametrize("m, hidden, inter, E, top_k, inter_sh", [
+    (1, 136, 5000, 24, 16, 0),       # 16 x 5000 gate/up rows: more than 16 rows for each of 148 x 16 warps
+    (1, 136, 5000, 24, 16, 5000),
+    (8, 136, 5000, 24, 8, 0),
+    (8, 136, 5000, 24, 8, 2504),
+    (13, 136, 5000, 24, 8, 0),
+    (13, 136, 5000, 24, 8, 2504),
+    (13, 2056, 64, 24, 8, 0),        # and of down rows
+    (13, 2056, 64, 24, 8, 64),
+    (24, 2056, 64, 24, 8, 64),
+    (8, 2056, 64, 32, 32, 64),       # more routed rows than the combining form holds
+])
+def test_several_rounds_of_tiles(m, hidden, inter, E, top_k, inter_sh):
+    c = make(m, hidden, inter, E, top_k, inter_sh)
+    check(c, call(c))
+    # a row has its bits alone and in the batch
+    part = call(dict(c, x=c["x"][m - 1:].contiguous()))
+    for a, b in zip(call(c), part):
+        assert torch.equal(a[m - 1:].view(torch.int32), b.view(torch.int32))
+
+
+@pytest.mark.parametrize("m", [2, 12])
+def test_experts_past_32_bit_offsets(m):
+    """Weights of more than 2^31 values each; the experts that no token chooses hold whatever was there."""
+    hidden, inter, E = 2048, 1032, 1024
+    assert E * inter * hidden > 2 ** 31
+    used = [3, 700, 1020, 1023]
+    small = make(m, hidden, inter, len(used), 3)
+    c = dict(small, W_router=torch.zeros(E, hidden, device="cuda").bfloat16(), bias=torch.full((E,), -5.0, device="cuda"))
+    c["W_router"][used], c["bias"][used] = small["W_router"], small["bias"]
+    for name in ("W_gate", "W_up", "W_down"):
+        c[name] = torch.empty((E, *small[name].shape[1:]), dtype=torch.bfloat16, device="cuda")
+        c[name][used] = small[name]
+    y, ids, w, logits = call(c)
+    back = torch.full((E,), -1, dtype=torch.int32, device="cuda")
+    back[used] = torch.arange(len(used), dtype=torch.int32, device="cuda")
+    check(small, (y, back[ids.long()], w, logits[:, used]))
