@@ -249,3 +249,40 @@ def test_rows_past_32_bit_offsets():
     for at in (0, 131072, 261888, m - 300):
         rows = slice(at, at + 300)
         check(dict(c, x=c["x"][rows], ids=c["ids"][rows]), y[rows])
+
+
+@pytest.mark.parametrize("at", [0, 300, 4999])
+def test_a_bad_id_among_many_row_tiles_leaves_y_unwritten(at):
+    m, n, k, rank, D = 5000, 4100, 72, 16, 7
+    c = make(m, n, k, rank, D, varied_ids(m, D, 5))
+    ws = torch.empty(moe.moe_matmul_lora_workspace(m, n, k, rank, D), dtype=torch.uint8, device="cuda")
+    y = torch.full((m, n), 5.0, device="cuda")
+    good = c["ids"][at].item()
+    c["ids"][at] = D
+    call(c, y=y, ws=ws)
+    assert moe.moe_check_status(ws) == 6 and (y == 5.0).all()
+    c["ids"][at] = good
+    check(c, call(c, y=y, ws=ws))
+    assert moe.moe_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("m, n", [(100, 520), (2500, 4100)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_replays_with_other_numbers_of_adapters(m, n, dtype):
+    """How a tile's adapters are added is decided on the device, by the ids of the replay."""
+    k, rank, D = 1024, 16, 64
+    c = make(m, n, k, rank, D, [-1] * m)
+    y = torch.empty((m, n), dtype=dtype, device="cuda")
+    ws = torch.empty(moe.moe_matmul_lora_workspace(m, n, k, rank, D), dtype=torch.uint8, device="cuda")
+    call(c, y=y, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c, y=y, ws=ws)
+    for used in (3, 64, 1, 20, 0):
+        c["ids"].copy_(torch.arange(m) % used if used else torch.full((m,), -1))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, y)
+        assert torch.equal(call(c, out_dtype=dtype), y)
+    del graph
