@@ -915,10 +915,10 @@ MOE_API moe_status_t moe_layer_decode(
 
 namespace {
 
-// K ranges of the adapters' first product on the streaming path: enough blocks
-// (an adapter per token, 32 rank rows on two SMs, one range each) for the SMs,
-// at least two steps of a block's 16 warps per range.  A function of the shape
-// alone.
+// K ranges of the adapters' first product on the streaming path: as many as give
+// every two blocks (16 rank rows each) of an adapter per token an SM, with at
+// least two steps of a block's 16 warps per range.  A function of the shape alone,
+// as the size of the workspace is.
 int lora_k_splits(long long m, int k, int rank) {
     if (m > moe::kLoraStreamMaxTokens) return 1;
     const long long blocks = m * ((rank + 31) / 32);

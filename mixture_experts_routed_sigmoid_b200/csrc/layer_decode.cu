@@ -30,9 +30,9 @@
 // lands, so its bits depend on its own token alone.
 //
 // Measured (graph replays; 256 experts, hidden 4096, inter 1536, top-8): 1
-// token 67 us (4.5 TB/s over the call, 5.6 while it streams), 8 tokens of 53
-// experts 346 (5.8), 32 tokens of 126 experts 772 (6.2), 32 tokens on 16 experts
-// 236 (2.6: their token rows, through L1 and L2).  Before the first expert byte: 9 us
+// token 64 us (4.7 TB/s over the call, 5.6 while it streams), 8 tokens of 53
+// experts 348 (5.8), 32 tokens of 126 experts 797 (6.0), 32 tokens on 16 experts
+// 227 (2.7: their token rows, through L1 and L2).  Before the first expert byte: 9 us
 // at 1 token, 21 at 32 (router 2.5 and 9, launch gap 2.6, routing 3.5 and 9).
 #include <climits>
 #include <math.h>

@@ -7,8 +7,8 @@
 //
 // A CTA pair owns a tile of 256 tokens x `bn` output columns (M = 256, N = bn
 // MMAs over both CTAs; each CTA loads its 128 tokens and its half of W's rows,
-// 128 bytes of K per stage).  The adapters enter as more columns of K behind
-// the projection's: for every adapter that occurs among the tile's tokens, its
+// 128 bytes of K per stage).  The adapters enter as more columns of K beside the
+// projection's: for every adapter that occurs among the tile's tokens, its
 // rank columns (rounded up to 16) once for each part of h, which is zero for the
 // tokens of other adapters.  So they cost parts * rank / k of the projection's
 // MMAs per adapter of a tile, and no pass over y.
@@ -35,8 +35,8 @@
 // MMAs.  Every wait is bounded.
 //
 // Bound by the tensor core: 4096 tokens of 4096 x 4096, 8 adapters of rank 16,
-// bf16 out: 118 us with the shrink kernel (1.16 PFLOP/s); 16384 tokens of 2048 x
-// 4096, 16 adapters of rank 64, f32 out: 261 us (1.05).
+// bf16 out: 122.5 us with the shrink kernel (1.12 PFLOP/s); 16384 tokens of 2048 x
+// 4096, 16 adapters of rank 64, f32 out: 254 us (1.08).
 #include <algorithm>
 
 #include "launch.h"

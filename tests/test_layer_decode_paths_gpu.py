@@ -1,5 +1,11 @@
 """moe_layer_decode on the paths that a call reaches by its size: router blocks
-of each form, several rounds of tiles."""
+of each form, several rounds of tiles.
+
+serving_reference.dot_gamma(k, parts) is 4 ceil(k / 1024) * 4 parts + 16 u (u =
+2^-24) of the sum of magnitudes.  A warp sums units of 64 columns in 4 * parts
+instructions of at most 4 u each, 16 parts u in all, and adds ceil(k / 64) of them,
+u each.  With c = ceil(k / 64) that is 16 parts + c, and the bound is at least 16
+parts ceil(c / 16) + 16: not below it for parts 1 and 3 at any c."""
 import pytest
 import torch
 

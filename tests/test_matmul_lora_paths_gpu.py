@@ -1,6 +1,14 @@
 """moe_matmul_lora on the paths that a call reaches by its size: the first
 product in several passes, row tiles one after another on a CTA pair, the
-adapters' part added token by token, K split over clusters."""
+adapters' part added token by token, K split over clusters.
+
+serving_reference.lora's bound counts one chain of k / 16 instructions of at most
+4 u (u = 2^-24) of the sum of magnitudes each, 16 u for what follows.  The kernels'
+chains are shorter.  Above 32 tokens: 64 or 48 instructions to a partial sum (256 u
+at most), whose k / 768 additions round by u each: below k / 4 u from k = 1024 on,
+and one chain of k / 16 before; the parts of up to 4 CTA pairs (8 CTAs in the first
+product) add by u each.  Up to 32: 4 instructions to a unit of 64 columns (16 u),
+k / 64 additions, 16 warps."""
 import pytest
 import torch
 
