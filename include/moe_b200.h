@@ -324,7 +324,7 @@ MOE_API moe_status_t moe_ffn_forward_shared(
  *            inter_sh = 0 and four NULLs
  *   y        f32 [m, hidden] (out)
  *   ids      int32 [m, top_k] (out); weights f32 [m, top_k] (out)
- *   logits   f32 [m, n_experts] (out)
+ *   logits   f32 [m, n_experts] (out); no output may overlap an input or another
  *   ws       moe_layer_decode_workspace() bytes, 256-byte aligned, no
  *            initialisation needed; calls that may overlap on the GPU need
  *            workspaces of their own
